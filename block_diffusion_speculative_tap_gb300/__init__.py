@@ -24,4 +24,5 @@ from .drafter import (  # noqa: F401
     verify_greedy,
     verify_sample,
 )
+from .target import PagedCache, Rows, logit_rules, token_counts  # noqa: F401
 from ._abi import DFlashError  # noqa: F401

@@ -32,6 +32,8 @@ E_UNSUPPORTED = -11
 STATUS_BAD_TOKEN = 1
 STATUS_TIMEOUT = 2
 STATUS_BAD_DRAFT = 4
+STATUS_BAD_PAGE = 8
+STATUS_BAD_ROWS = 16
 
 LAYER_FULL = 0
 LAYER_SLIDING = 1
@@ -40,6 +42,11 @@ VARIANT_2 = 2
 VERIFY_GREEDY = 0
 VERIFY_SAMPLE = 1
 FUSE_INJECT_KV = 1
+PAGES_BF16 = 0
+PAGES_FP4 = 1
+MASK_CAUSAL = 0
+MASK_BLOCK = 1
+MASK_TREE = 2
 
 
 class Config(C.Structure):
@@ -97,6 +104,50 @@ class Weights(C.Structure):
     ]
 
 
+class Pages(C.Structure):
+    _fields_ = [
+        ("format", C.c_int32),
+        ("n_pages", C.c_int32),
+        ("page_size", C.c_int32),
+        ("n_kv_heads", C.c_int32),
+        ("head_dim", C.c_int32),
+        ("streams", C.c_int32),
+        ("table_cols", C.c_int32),
+        ("k", C.c_void_p),
+        ("v", C.c_void_p),
+        ("k_scale", C.c_void_p),
+        ("v_scale", C.c_void_p),
+        ("table", C.c_void_p),
+    ]
+
+
+class RowsDesc(C.Structure):
+    _fields_ = [
+        ("rows", C.c_int32),
+        ("max_rows", C.c_int32),
+        ("row_start", C.c_void_p),
+        ("lens", C.c_void_p),
+        ("depth", C.c_void_p),
+    ]
+
+
+class Rules(C.Structure):
+    _fields_ = [
+        ("counts", C.c_void_p),
+        ("tokens", C.c_void_p),
+        ("node_mask", C.c_void_p),
+        ("mask_ld", C.c_int32),
+        ("n_bias", C.c_int32),
+        ("repetition", C.c_void_p),
+        ("frequency", C.c_void_p),
+        ("presence", C.c_void_p),
+        ("bias_start", C.c_void_p),
+        ("bias_ids", C.c_void_p),
+        ("bias_vals", C.c_void_p),
+        ("grammar", C.c_void_p),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -148,6 +199,14 @@ def _load():
     fn("dflash_verify_workspace_bytes", C.c_int, C.c_int, C.c_int, C.c_int, P(sz))
     fn("dflash_verify", C.c_int, C.c_int, C.c_int, C.c_int, vp, C.c_int, vp, vp, vp, C.c_float, vp, vp, vp, sz, vp)
     fn("dflash_verify_sample_noalloc", C.c_int, C.c_int, C.c_int, vp, C.c_int, vp, vp, vp, C.c_float, vp, vp, vp)
+    fn("dflash_page_append", C.c_int, P(Pages), P(RowsDesc), vp, i64, vp, i64, vp, C.c_int, C.c_int, vp, i64, vp, i64,
+       vp, vp)
+    fn("dflash_page_read", C.c_int, P(Pages), P(RowsDesc), vp, i64, vp, i64, vp, vp)
+    fn("dflash_page_attention_workspace_bytes", C.c_int, P(Pages), P(RowsDesc), C.c_int, P(sz))
+    fn("dflash_page_attention", C.c_int, P(Pages), P(RowsDesc), C.c_int, vp, i64, C.c_float, C.c_int, C.c_int, C.c_int,
+       vp, C.c_int, vp, i64, vp, vp, sz, vp)
+    fn("dflash_token_counts", C.c_int, C.c_int, C.c_int, vp, vp, vp, C.c_int, i64, C.c_int, vp)
+    fn("dflash_logit_rules", C.c_int, C.c_int, C.c_int, C.c_int, vp, P(Rules), vp, vp)
     fn("dflash_trace_enable", C.c_int, C.c_int)
     fn("dflash_trace_count", C.c_int)
     fn("dflash_trace_get", C.c_int, C.c_int, P(C.c_char_p), P(C.c_float), P(C.c_double), P(C.c_double))
@@ -192,6 +251,12 @@ EXPORTED = [
     "dflash_verify_workspace_bytes",
     "dflash_verify",
     "dflash_verify_sample_noalloc",
+    "dflash_page_append",
+    "dflash_page_read",
+    "dflash_page_attention_workspace_bytes",
+    "dflash_page_attention",
+    "dflash_token_counts",
+    "dflash_logit_rules",
     "dflash_trace_enable",
     "dflash_trace_count",
     "dflash_trace_get",

@@ -1,0 +1,239 @@
+// Host side of the target's verification pass: argument checks, work split
+// and launches of the paged cache, its attention and the logit rules. See
+// include/dflash.h for the contract of every function.
+#include <algorithm>
+
+#include "internal.h"
+#include "pages.h"
+#include "rules.h"
+
+using namespace dfl;
+
+namespace {
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+constexpr int kSms = 152;
+
+int check_pages(const dflash_pages* c) {
+  if (!c) return DFLASH_E_INVALID_ARG;
+  if (c->format != DFLASH_PAGES_BF16 && c->format != DFLASH_PAGES_FP4) return DFLASH_E_INVALID_ARG;
+  if (c->head_dim != 32 && c->head_dim != 64 && c->head_dim != 128) return DFLASH_E_SHAPE;
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128) return DFLASH_E_SHAPE;
+  if (c->n_kv_heads < 1 || c->n_kv_heads > 65535) return DFLASH_E_SHAPE;
+  if (c->n_pages < 1 || c->streams < 0 || c->table_cols < 1) return DFLASH_E_INVALID_ARG;
+  if (static_cast<int64_t>(c->table_cols) * c->page_size > 0x3fffffff) return DFLASH_E_CAPACITY;
+  // a row of the pool is a coordinate of 31 bits
+  if (static_cast<int64_t>(c->n_pages) * c->n_kv_heads * c->page_size > 0x7fffffff) return DFLASH_E_CAPACITY;
+  if (c->streams > 0 && !c->table) return DFLASH_E_INVALID_ARG;
+  if (!c->k || !c->v || !aligned(c->k, 128) || !aligned(c->v, 128)) return DFLASH_E_INVALID_ARG;
+  if (c->format == DFLASH_PAGES_FP4 &&
+      (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16)))
+    return DFLASH_E_INVALID_ARG;
+  return DFLASH_OK;
+}
+
+int check_rows(const dflash_pages* c, const dflash_rows* r) {
+  if (!r || r->rows < 0 || r->max_rows < 0 || r->rows > 0x3fffffff || r->max_rows > 0x3fffffff)
+    return DFLASH_E_INVALID_ARG;
+  if (c->streams > 0 && (!r->row_start || !r->lens)) return DFLASH_E_INVALID_ARG;
+  return DFLASH_OK;
+}
+
+bool nothing(const dflash_pages* c, const dflash_rows* r) { return c->streams == 0 || r->rows == 0 || r->max_rows == 0; }
+
+PagesArgs pages_args(const dflash_pages& c) {
+  PagesArgs a{};
+  a.k = static_cast<uint8_t*>(c.k);
+  a.v = static_cast<uint8_t*>(c.v);
+  a.ks = static_cast<uint8_t*>(c.k_scale);
+  a.vs = static_cast<uint8_t*>(c.v_scale);
+  a.table = c.table;
+  a.n_pages = c.n_pages;
+  a.page = c.page_size;
+  a.page_log2 = c.page_size == 16 ? 4 : c.page_size == 32 ? 5 : c.page_size == 64 ? 6 : 7;
+  a.nkv = c.n_kv_heads;
+  a.d = c.head_dim;
+  a.S = c.streams;
+  a.cols = c.table_cols;
+  return a;
+}
+
+RowsArgs rows_args(const dflash_pages& c, const dflash_rows& r, int32_t* status) {
+  RowsArgs a{};
+  a.row_start = r.row_start;
+  a.lens = r.lens;
+  a.depth = r.depth;
+  a.T = r.rows;
+  a.max_rows = r.max_rows;
+  a.S = c.streams;
+  a.cap = c.table_cols * c.page_size;
+  a.status = status;
+  return a;
+}
+
+// Rows of `heads` heads, `ld` elements apart, in 16-byte pieces.
+bool good_rows(const void* p, int64_t ld, int64_t heads, int d) {
+  return p && aligned(p, 16) && ld >= heads * d && ld % 8 == 0;
+}
+
+size_t attention_ws(const PagePlan& p, const dflash_pages& c) {
+  const size_t rows = static_cast<size_t>(p.slots) * c.n_kv_heads * p.tile;
+  return (rows * c.head_dim + rows * 2) * sizeof(float);
+}
+
+int check_heads(const dflash_pages* c, int nq) {
+  return nq < 1 || nq % c->n_kv_heads || nq / c->n_kv_heads > DFLASH_MAX_PAGE_GROUP ? DFLASH_E_SHAPE : DFLASH_OK;
+}
+
+// the grid's x axis holds the call's items
+int check_items(const PagePlan& p) { return p.items > 0x7fffffff ? DFLASH_E_SHAPE : DFLASH_OK; }
+
+}  // namespace
+
+extern "C" {
+
+int dflash_page_append(const dflash_pages* c, const dflash_rows* r, const void* k, int64_t k_ld, const void* v,
+                       int64_t v_ld, const float* rope, int rope_rows, int n_q_heads, const void* q, int64_t q_ld,
+                       void* q_out, int64_t q_out_ld, int32_t* status, dflash_stream_t stream) {
+  int rc = check_pages(c);
+  if (!rc) rc = check_rows(c, r);
+  if (rc) return rc;
+  if (rope ? (rope_rows < 1 || !aligned(rope, 16)) : rope_rows != 0) return DFLASH_E_INVALID_ARG;
+  if (n_q_heads < 0 || (n_q_heads == 0) != (q == nullptr) || (q == nullptr) != (q_out == nullptr))
+    return DFLASH_E_INVALID_ARG;
+  if (q && !rope) return DFLASH_E_INVALID_ARG;
+  if (nothing(c, r)) return DFLASH_OK;
+  const int d = c->head_dim;
+  if (!good_rows(k, k_ld, c->n_kv_heads, d) || !good_rows(v, v_ld, c->n_kv_heads, d)) return DFLASH_E_INVALID_ARG;
+  if (q && (!good_rows(q, q_ld, n_q_heads, d) || !good_rows(q_out, q_out_ld, n_q_heads, d)))
+    return DFLASH_E_INVALID_ARG;
+  return launch_page_append(pages_args(*c), rows_args(*c, *r, status), static_cast<const __nv_bfloat16*>(k), k_ld,
+                            static_cast<const __nv_bfloat16*>(v), v_ld, reinterpret_cast<const float2*>(rope),
+                            rope_rows, static_cast<const __nv_bfloat16*>(q), q_ld, static_cast<__nv_bfloat16*>(q_out),
+                            q_out_ld, n_q_heads, c->format == DFLASH_PAGES_FP4, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int dflash_page_read(const dflash_pages* c, const dflash_rows* r, void* k, int64_t k_ld, void* v, int64_t v_ld,
+                     int32_t* status, dflash_stream_t stream) {
+  int rc = check_pages(c);
+  if (!rc) rc = check_rows(c, r);
+  if (rc) return rc;
+  if (nothing(c, r)) return DFLASH_OK;
+  const int d = c->head_dim;
+  if (!good_rows(k, k_ld, c->n_kv_heads, d) || !good_rows(v, v_ld, c->n_kv_heads, d)) return DFLASH_E_INVALID_ARG;
+  return launch_page_read(pages_args(*c), rows_args(*c, *r, status), static_cast<__nv_bfloat16*>(k), k_ld,
+                          static_cast<__nv_bfloat16*>(v), v_ld, c->format == DFLASH_PAGES_FP4,
+                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+int dflash_page_attention_workspace_bytes(const dflash_pages* c, const dflash_rows* r, int n_q_heads, size_t* bytes) {
+  int rc = check_pages(c);
+  if (!rc) rc = check_rows(c, r);
+  if (!rc) rc = check_heads(c, n_q_heads);
+  if (rc) return rc;
+  if (!bytes) return DFLASH_E_INVALID_ARG;
+  *bytes = 0;
+  if (nothing(c, r)) return DFLASH_OK;
+  const PagePlan p = page_attention_plan(*c, *r, n_q_heads);
+  rc = check_items(p);
+  if (!rc) *bytes = attention_ws(p, *c);
+  return rc;
+}
+
+int dflash_page_attention(const dflash_pages* c, const dflash_rows* r, int n_q_heads, const void* q, int64_t q_ld,
+                          float scale, int window, int sinks, int mask_mode, const uint32_t* mask, int mask_ld,
+                          void* out, int64_t out_ld, int32_t* status, void* ws, size_t ws_bytes,
+                          dflash_stream_t stream) {
+  int rc = check_pages(c);
+  if (!rc) rc = check_rows(c, r);
+  if (!rc) rc = check_heads(c, n_q_heads);
+  if (rc) return rc;
+  if (!(scale > 0.f) || scale > 3.0e38f || window < 0 || sinks < 0) return DFLASH_E_INVALID_ARG;
+  if (mask_mode != DFLASH_MASK_CAUSAL && mask_mode != DFLASH_MASK_BLOCK && mask_mode != DFLASH_MASK_TREE)
+    return DFLASH_E_INVALID_ARG;
+  if (nothing(c, r)) return DFLASH_OK;
+  if (mask_mode == DFLASH_MASK_TREE &&
+      (!mask || !aligned(mask, 4) || static_cast<int64_t>(mask_ld) * 32 < r->max_rows))
+    return DFLASH_E_INVALID_ARG;
+  if (!good_rows(q, q_ld, n_q_heads, c->head_dim) || !good_rows(out, out_ld, n_q_heads, c->head_dim))
+    return DFLASH_E_INVALID_ARG;
+  const PagePlan p = page_attention_plan(*c, *r, n_q_heads);
+  rc = check_items(p);
+  if (rc) return rc;
+  const size_t need = attention_ws(p, *c);
+  if (need > 0 && (!ws || ws_bytes < need || !aligned(ws, 16))) return DFLASH_E_WORKSPACE;
+  PageAttnArgs a{};
+  a.c = pages_args(*c);
+  a.r = rows_args(*c, *r, status);
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.q_ld = q_ld;
+  a.out_ld = out_ld;
+  a.mask = mask;
+  a.mask_ld = mask_ld;
+  a.mode = mask_mode;
+  a.window = window;
+  a.sinks = window > 0 ? sinks : 0;
+  a.nq = n_q_heads;
+  a.G = n_q_heads / c->n_kv_heads;
+  a.scale = scale * 1.4426950408889634f;
+  a.unit = p.unit;
+  a.tile = p.tile;
+  a.target = p.target;
+  a.min_units = p.min_units;
+  a.slots = p.slots;
+  a.part_o = static_cast<float*>(ws);
+  a.part_ml = a.part_o ? a.part_o + static_cast<size_t>(p.slots) * c->n_kv_heads * p.tile * c->head_dim : nullptr;
+  return launch_page_attention(a, p, c->format == DFLASH_PAGES_FP4, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int dflash_token_counts(int streams, int vocab, void* counts, const int32_t* tokens, const int32_t* row_start,
+                        int per_stream, int64_t total, int prompt, dflash_stream_t stream) {
+  if (streams < 0 || vocab < 8 || vocab % 8 || total < 0 || total > (1ll << 38)) return DFLASH_E_INVALID_ARG;
+  if (prompt != 0 && prompt != 1) return DFLASH_E_INVALID_ARG;
+  if (!row_start && (per_stream < 1 || total > static_cast<int64_t>(streams) * per_stream)) return DFLASH_E_INVALID_ARG;
+  if (streams == 0 || total == 0) return DFLASH_OK;
+  if (!counts || !tokens || !aligned(counts, 16)) return DFLASH_E_INVALID_ARG;
+  return launch_token_counts(static_cast<uint16_t*>(counts), tokens, row_start, streams, vocab, per_stream, total,
+                             prompt, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int dflash_logit_rules(int streams, int rows, int vocab, const void* logits, const dflash_rules* rules, void* out,
+                       dflash_stream_t stream) {
+  if (streams < 0 || rows < 0 || rows > DFLASH_MAX_TREE_NODES || vocab < 8 || vocab % 8 || !rules)
+    return DFLASH_E_INVALID_ARG;
+  const dflash_rules& u = *rules;
+  if ((u.repetition || u.frequency || u.presence) && !u.counts) return DFLASH_E_INVALID_ARG;
+  if (u.tokens && !u.counts) return DFLASH_E_INVALID_ARG;
+  if (u.node_mask && (!u.tokens || static_cast<int64_t>(u.mask_ld) * 32 < rows)) return DFLASH_E_INVALID_ARG;
+  if ((u.bias_start == nullptr) != (u.bias_ids == nullptr) || (u.bias_start == nullptr) != (u.bias_vals == nullptr) ||
+      u.n_bias < 0)
+    return DFLASH_E_INVALID_ARG;
+  if (u.counts && !aligned(u.counts, 16)) return DFLASH_E_INVALID_ARG;
+  if (u.grammar && !aligned(u.grammar, 4)) return DFLASH_E_INVALID_ARG;
+  if (streams == 0 || rows == 0) return DFLASH_OK;
+  if (!logits || !out || !aligned(logits, 16) || !aligned(out, 16)) return DFLASH_E_INVALID_ARG;
+  RulesArgs a{};
+  a.in = static_cast<const __nv_bfloat16*>(logits);
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.S = streams;
+  a.N = rows;
+  a.V = vocab;
+  a.words = (vocab + 31) / 32;
+  a.mask_ld = u.mask_ld;
+  a.n_bias = u.n_bias;
+  a.counts = static_cast<const uint16_t*>(u.counts);
+  a.tokens = u.tokens;
+  a.node_mask = u.node_mask;
+  a.repetition = u.repetition;
+  a.frequency = u.frequency;
+  a.presence = u.presence;
+  a.bias_start = u.bias_start;
+  a.bias_ids = u.bias_ids;
+  a.bias_vals = u.bias_vals;
+  a.grammar = u.grammar;
+  return launch_logit_rules(a, kSms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,264 @@
+"""Wrappers of the target's verification pass (marshalling only): the paged
+K/V cache, its attention and the logit rules of include/dflash.h.
+
+Tensors are checked for type, device and layout here; shapes and limits are
+checked by the library. Workspaces are allocated a call on the current stream,
+so calls on several streams, and captured graphs, never share one.
+"""
+from __future__ import annotations
+
+import ctypes as C
+import math
+
+import torch
+
+from . import _abi as A
+from ._abi import check, lib
+
+__all__ = ["PagedCache", "Rows", "token_counts", "logit_rules"]
+
+_MODES = {"causal": A.MASK_CAUSAL, "block": A.MASK_BLOCK}
+
+
+def _need(t, dtype, dev, what):
+    if t.dtype != dtype or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor on {dev}")
+    return t.data_ptr()
+
+
+def _on(dev):
+    """The current stream of the tensors' device, which has to be the current one."""
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {dev}: expected the current CUDA device")
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _heads(t, dtype, dev, dim, what):
+    """(pointer, row stride, heads) of rows [T, heads, dim] whose heads are dense."""
+    if t.dtype != dtype or t.device != dev or t.dim() != 3 or t.shape[2] != dim:
+        raise ValueError(f"{what}: expected {dtype} [rows, heads, {dim}] on {dev}")
+    T, h, _ = t.shape
+    st = t.stride()
+    if st[2] != 1 or (h > 1 and st[1] != dim):
+        raise ValueError(f"{what}: the heads of a row must be dense")
+    return t.data_ptr(), (st[0] if T > 1 else h * dim), h
+
+
+class Rows:
+    """A ragged batch of rows behind the streams' committed lengths (dflash_rows).
+
+    row_start int32 [S + 1], lens int32 [S] and optionally depth int32 [rows],
+    on the GPU; read when a call's kernels run, so a captured call follows
+    their later contents. max_rows: a bound of every stream's rows."""
+
+    def __init__(self, row_start, lens, rows: int, max_rows: int, depth=None):
+        dev = row_start.device
+        self.device = dev
+        self.streams = lens.numel()
+        if row_start.numel() != self.streams + 1:
+            raise ValueError("row_start: one entry more than lens")
+        if depth is not None and depth.numel() < rows:
+            raise ValueError("depth: one entry a row")
+        self.rows, self.max_rows = int(rows), int(max_rows)
+        self.row_start, self.lens, self.depth = row_start, lens, depth
+        i32 = torch.int32
+        self.desc = A.RowsDesc(
+            self.rows, self.max_rows, _need(row_start, i32, dev, "row_start"), _need(lens, i32, dev, "lens"),
+            _need(depth, i32, dev, "depth") if depth is not None else None,
+        )
+        self._ref = C.byref(self.desc)
+
+
+class PagedCache:
+    """One layer's paged K/V cache (dflash_pages).
+
+    k, v: bf16 [n_pages, n_kv, page_size, d], or uint8 [n_pages, n_kv,
+    page_size, d / 2] of 4-bit codes with k_scale, v_scale uint8 (e4m3 bytes)
+    [n_pages, n_kv, page_size, d / 16]. table: int32 [S, max_pages]. status:
+    None, or an int32 [1] GPU tensor that collects DFLASH_STATUS_* bits."""
+
+    def __init__(self, k, v, table, k_scale=None, v_scale=None, status=None):
+        dev = k.device
+        self.fp4 = k_scale is not None
+        dt = torch.uint8 if self.fp4 else torch.bfloat16
+        if k.dim() != 4 or v.shape != k.shape or table.dim() != 2:
+            raise ValueError("k, v: [n_pages, n_kv, page_size, row] of one shape; table: [S, max_pages]")
+        n, h, page, row = k.shape
+        d = row * 2 if self.fp4 else row
+        self.k, self.v, self.table, self.k_scale, self.v_scale, self.status = k, v, table, k_scale, v_scale, status
+        self.device, self.streams, self.n_kv, self.head_dim = dev, table.shape[0], h, d
+        if self.fp4:
+            for s in (k_scale, v_scale):
+                if s is None or tuple(s.shape) != (n, h, page, d // 16):
+                    raise ValueError("k_scale, v_scale: [n_pages, n_kv, page_size, d / 16]")
+        self.desc = A.Pages(
+            A.PAGES_FP4 if self.fp4 else A.PAGES_BF16, n, page, h, d, table.shape[0], table.shape[1],
+            _need(k, dt, dev, "k"), _need(v, dt, dev, "v"),
+            _need(k_scale, torch.uint8, dev, "k_scale") if self.fp4 else None,
+            _need(v_scale, torch.uint8, dev, "v_scale") if self.fp4 else None,
+            _need(table, torch.int32, dev, "table"),
+        )
+        self._ref = C.byref(self.desc)
+        self._status = _need(status, torch.int32, dev, "status") if status is not None else None
+
+    def _check(self, rows):
+        if rows.device != self.device or rows.streams != self.streams:
+            raise ValueError("rows: another device, or another number of streams than the table's")
+        return _on(self.device)
+
+    def _rows_of(self, t, rows, what, n=None):
+        p, ld, h = _heads(t, torch.bfloat16, self.device, self.head_dim, what)
+        if t.shape[0] < rows.rows or (n is not None and h != n):
+            raise ValueError(f"{what}: {rows.rows} rows of {n if n is not None else h} heads")
+        return p, ld, h
+
+    def append(self, rows: Rows, k, v, rope=None, q=None, q_out=None):
+        """dflash_page_append: k, v bf16 [rows, n_kv, d] go to the rows' slots, keys
+        (and q bf16 [rows, n_q, d]) rotated by rope fp32 [positions, d / 2, 2].
+        Returns the rotated queries (q_out if given), or None without q."""
+        stream = self._check(rows)
+        kp, kl, _ = self._rows_of(k, rows, "k", self.n_kv)
+        vp, vl, _ = self._rows_of(v, rows, "v", self.n_kv)
+        rp, rn = None, 0
+        if rope is not None:
+            rn = rope.shape[0]
+            if rope.numel() != rn * self.head_dim:
+                raise ValueError("rope: fp32 [positions, d / 2, 2]")
+            rp = _need(rope, torch.float32, self.device, "rope")
+        qp, ql, nq, op, ol = None, 0, 0, None, 0
+        if q is not None:
+            qp, ql, nq = self._rows_of(q, rows, "q")
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            op, ol, _ = self._rows_of(q_out, rows, "q_out", nq)
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        check(
+            lib.dflash_page_append(self._ref, rows._ref, kp, kl, vp, vl, rp, rn, nq, qp, ql, op, ol, self._status,
+                                   stream),
+            "dflash_page_append",
+        )
+        return q_out
+
+    def read(self, rows: Rows, k=None, v=None):
+        """dflash_page_read: the values of the rows' slots, bf16 [rows, n_kv, d] each."""
+        stream = self._check(rows)
+        shape = (rows.rows, self.n_kv, self.head_dim)
+        k = torch.empty(shape, dtype=torch.bfloat16, device=self.device) if k is None else k
+        v = torch.empty(shape, dtype=torch.bfloat16, device=self.device) if v is None else v
+        kp, kl, _ = self._rows_of(k, rows, "k", self.n_kv)
+        vp, vl, _ = self._rows_of(v, rows, "v", self.n_kv)
+        check(lib.dflash_page_read(self._ref, rows._ref, kp, kl, vp, vl, self._status, stream), "dflash_page_read")
+        return k, v
+
+    def workspace_bytes(self, rows: Rows, n_q: int) -> int:
+        nb = C.c_size_t()
+        check(lib.dflash_page_attention_workspace_bytes(self._ref, rows._ref, n_q, C.byref(nb)),
+              "dflash_page_attention_workspace_bytes")
+        return nb.value
+
+    def attend(self, rows: Rows, q, window=0, sinks=0, mask="causal", scale=None, out=None, ws=None):
+        """dflash_page_attention of q bf16 [rows, n_q, d]. mask: "causal", "block", or
+        the rows' mask words int32 [rows, words] (tree_build's node_mask, a row of
+        words a row of the batch). scale: 1 / sqrt(d) unless given. ws: a uint8
+        workspace of workspace_bytes(); allocated a call unless given."""
+        stream = self._check(rows)
+        qp, ql, nq = self._rows_of(q, rows, "q")
+        mode, mp, mld = A.MASK_TREE, None, 0
+        if isinstance(mask, str):
+            if mask not in _MODES:
+                raise ValueError('mask: "causal", "block" or mask words')
+            mode = _MODES[mask]
+        else:
+            if mask.dim() != 2 or mask.shape[0] < rows.rows:
+                raise ValueError("mask: int32 [rows, words]")
+            mp, mld = _need(mask, torch.int32, self.device, "mask"), mask.shape[1]
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        op, ol, _ = self._rows_of(out, rows, "out", nq)
+        if ws is None:
+            nbytes = self.workspace_bytes(rows, nq)
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device) if nbytes else None
+        wp, wn = (_need(ws, torch.uint8, self.device, "ws"), ws.numel()) if ws is not None else (None, 0)
+        check(
+            lib.dflash_page_attention(
+                self._ref, rows._ref, nq, qp, ql, scale if scale is not None else 1.0 / math.sqrt(self.head_dim),
+                window, sinks, mode, mp, mld, op, ol, self._status, wp, wn, stream,
+            ),
+            "dflash_page_attention",
+        )
+        return out
+
+
+def token_counts(counts, tokens, row_start=None, prompt=False):
+    """dflash_token_counts: add tokens to counts int16 [S, V] (bit 15 prompt, bits
+    0..14 output count). tokens: int32, ragged with row_start int32 [S + 1], or
+    [S, n] (verify's out_tokens as they are: -1s are skipped). Returns counts."""
+    dev = counts.device
+    stream = _on(dev)
+    S, V = counts.shape
+    total, per = tokens.numel(), 0
+    if row_start is None:
+        if tokens.dim() != 2 or tokens.shape[0] != S:
+            raise ValueError("tokens: [S, n], or row_start")
+        per = max(1, tokens.shape[1])
+    elif row_start.numel() != S + 1:
+        raise ValueError("row_start: [S + 1]")
+    check(
+        lib.dflash_token_counts(
+            S, V, _need(counts, torch.int16, dev, "counts"), _need(tokens, torch.int32, dev, "tokens"),
+            _need(row_start, torch.int32, dev, "row_start") if row_start is not None else None, per, total,
+            int(bool(prompt)), stream,
+        ),
+        "dflash_token_counts",
+    )
+    return counts
+
+
+def logit_rules(logits, counts=None, tokens=None, node_mask=None, repetition=None, frequency=None, presence=None,
+                bias=None, grammar=None, out=None):
+    """dflash_logit_rules on logits bf16 [S, rows, V] (verify's [S, 16, V], a tree's
+    [S, N, V]). counts int16 [S, V]; tokens int32 [S, rows]; node_mask int32 [S,
+    rows, words]; repetition, frequency, presence fp32 [S]; bias: (start int32
+    [S + 1], ids int32, values fp32); grammar int32 [S, rows, ceil(V / 32)].
+    Returns out (a new tensor unless given; out may be logits)."""
+    dev = logits.device
+    stream = _on(dev)
+    if logits.dim() != 3:
+        raise ValueError("logits: [S, rows, V]")
+    S, N, V = logits.shape
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+
+    def opt(t, dtype, shape, what):
+        if t is None:
+            return None
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{what}: expected {list(shape)}, got {list(t.shape)}")
+        return _need(t, dtype, dev, what)
+
+    i32, f32 = torch.int32, torch.float32
+    u = A.Rules()
+    u.counts = opt(counts, torch.int16, (S, V), "counts")
+    u.tokens = opt(tokens, i32, (S, N), "tokens")
+    if node_mask is not None:
+        u.mask_ld = node_mask.shape[-1]
+        u.node_mask = opt(node_mask, i32, (S, N, u.mask_ld), "node_mask")
+    u.repetition = opt(repetition, f32, (S,), "repetition")
+    u.frequency = opt(frequency, f32, (S,), "frequency")
+    u.presence = opt(presence, f32, (S,), "presence")
+    if bias is not None:
+        start, ids, vals = bias
+        u.n_bias = ids.numel()
+        u.bias_start = opt(start, i32, (S + 1,), "bias start")
+        u.bias_ids = opt(ids, i32, (u.n_bias,), "bias ids")
+        u.bias_vals = opt(vals, f32, (u.n_bias,), "bias values")
+        if u.n_bias == 0:  # an empty list has no storage
+            u.bias_start = u.bias_ids = u.bias_vals = None
+    u.grammar = opt(grammar, i32, (S, N, (V + 31) // 32), "grammar")
+    check(
+        lib.dflash_logit_rules(S, N, V, _need(logits, torch.bfloat16, dev, "logits"), C.byref(u),
+                               opt(out, torch.bfloat16, (S, N, V), "out"), stream),
+        "dflash_logit_rules",
+    )
+    return out

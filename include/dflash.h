@@ -13,6 +13,11 @@
  * and the rows after them: dflash_draft_stop (min-p stop),
  * dflash_select_path (the DFlash2 candidate-path selector), dflash_tree_build
  * and dflash_tree_verify (tree drafting and greedy tree verification).
+ * Between drafting and verification, for the target's own layers:
+ * dflash_page_append, dflash_page_attention and dflash_page_read (a paged K/V
+ * cache in bf16 or 4 bits and the drafted rows' attention over it), and
+ * dflash_token_counts and dflash_logit_rules (penalties, biases and grammar
+ * masks on the target's scores).
  *
  * Sources, cited by page title and section:
  *   [TF1851]  TensorFold pull request #1851, "qwen27 dflash: read and run the
@@ -76,7 +81,9 @@ enum {
 enum {
   DFLASH_STATUS_BAD_TOKEN = 1,   /* an anchor id outside [0, vocab): row read as id 0 */
   DFLASH_STATUS_TIMEOUT = 2,     /* a bounded mbarrier wait expired; results invalid */
-  DFLASH_STATUS_BAD_DRAFT = 4    /* a draft id outside [0, vocab) in dflash_verify */
+  DFLASH_STATUS_BAD_DRAFT = 4,   /* a draft id outside [0, vocab) in dflash_verify */
+  DFLASH_STATUS_BAD_PAGE = 8,    /* a slot needed from a table entry that is no page */
+  DFLASH_STATUS_BAD_ROWS = 16    /* row_start, lens or depth outside what dflash_rows allows */
 };
 
 #define DFLASH_MAX_TAPS 8
@@ -432,6 +439,176 @@ int dflash_tree_verify_workspace_bytes(int streams, int nodes, size_t* bytes);
 int dflash_tree_verify(int streams, int depth, const int32_t* widths, int vocab, const int32_t* node_tokens,
                        const void* target_logits, int32_t* accept_len, int32_t* out_tokens, int32_t* accept_node,
                        void* ws, size_t ws_bytes, dflash_stream_t stream);
+
+/* ---------------------------------------------------------------- paged target cache
+ * One target layer's K/V cache for the verification pass: the drafted rows
+ * (the anchor and its block, or a draft tree's nodes) are appended behind
+ * their stream's committed length and attend over it before dflash_verify or
+ * dflash_tree_verify decides how many stay. A stream's slots lie in pages
+ * anywhere in a pool; slot c of stream s is slot c % page_size of page
+ * table[s][c / page_size]. Rejected rows need no removal: the next round's
+ * rows take their slots.
+ *
+ * dflash_pages: the pool and the table (host struct; all its pointers are
+ * device memory of the caller).
+ *   format BF16: k, v = bf16 [n_pages][n_kv_heads][page_size][head_dim].
+ *   format FP4: k, v = bytes [n_pages][n_kv_heads][page_size][head_dim / 2],
+ *     byte i of a row holding dims 2i (low nibble) and 2i + 1 (high nibble) as
+ *     e2m1 codes, and k_scale, v_scale = bytes
+ *     [n_pages][n_kv_heads][page_size][head_dim / 16], the e4m3 scale of each
+ *     group of 16 dims. A value is code * scale.
+ *   k, v 128-byte aligned, scales 16-byte aligned; head_dim 32, 64 or 128;
+ *   page_size 16, 32, 64 or 128; at most 2^31 - 1 rows (n_pages * n_kv_heads
+ *   * page_size) in a pool and 2^30 - 1 slots a stream.
+ *   table: int32 [streams][table_cols]. Entries that no needed slot lies in
+ *   are not read as pages (any value will do). Pages may be shared by streams
+ *   that only read them; a page that is appended to belongs to one stream.
+ *
+ * dflash_rows: a ragged batch, stream s with rows row_start[s] ..
+ * row_start[s + 1] - 1 of the row buffers, the j-th of them in slot
+ * lens[s] + j (lens: the committed length before the batch, as
+ * dflash_state_length counts it). A row's position (its rotation, and where
+ * its window starts) is lens[s] + j, or lens[s] + depth[row] where depth is
+ * given (a tree's node_depth). row_start ascends from 0 on; max_rows is at
+ * least every stream's rows and `rows` at least row_start[streams] (buffers
+ * may be longer: rows past the last stream are neither read nor written). A
+ * stream may have no rows.
+ *
+ * What only the device can see wrong is flagged in *status (device int32,
+ * DFLASH_STATUS_BAD_PAGE / BAD_ROWS OR-ed in, never cleared; NULL: not
+ * reported) and never read or written through: a slot without a page is not
+ * stored, not seen, and left as it was in an output; results of a stream so
+ * flagged are not valid. */
+enum { DFLASH_PAGES_BF16 = 0, DFLASH_PAGES_FP4 = 1 };
+#define DFLASH_MAX_PAGE_GROUP 128 /* query heads a kv head */
+typedef struct dflash_pages {
+  int32_t format;
+  int32_t n_pages, page_size, n_kv_heads, head_dim;
+  int32_t streams, table_cols;
+  void *k, *v;
+  void *k_scale, *v_scale; /* FP4 only */
+  const int32_t* table;
+} dflash_pages;
+typedef struct dflash_rows {
+  int32_t rows, max_rows;
+  const int32_t* row_start; /* [streams + 1] */
+  const int32_t* lens;      /* [streams] */
+  const int32_t* depth;     /* [rows] or NULL */
+} dflash_rows;
+
+/* Append the rows' keys and values to the cache, rotating the keys and the
+ * rows' queries on the way.
+ *   k, v: device bf16 [rows][n_kv_heads][head_dim], rows k_ld / v_ld elements
+ *     apart (multiples of 8; the projections' output can be read in place).
+ *   rope: device fp32 [rope_rows][head_dim / 2][2], (cos, sin) of every
+ *     position; 16-byte aligned. y_i = x_i cos - x_{i+d/2} sin,
+ *     y_{i+d/2} = x_{i+d/2} cos + x_i sin, each operation rounded to fp32, y
+ *     to bf16. NULL (rope_rows 0): keys are stored as they are.
+ *   q, q_out: device bf16 [rows][n_q_heads][head_dim] (strides as k), rotated
+ *     alike; q_out may be q. NULL, with n_q_heads 0, for keys alone.
+ * FP4: the bf16 value y goes to the group's scale s = e4m3(max |y| / 6) (at
+ * most 448, to nearest even; a group under 2^-10 * 6 becomes zeros) and the
+ * code e2m1(y / s) (to nearest even, beyond 6 clamped; a NaN becomes 6 s).
+ * A row at or past rope_rows is flagged BAD_ROWS and skipped. */
+int dflash_page_append(const dflash_pages* pages, const dflash_rows* rows, const void* k, int64_t k_ld, const void* v,
+                       int64_t v_ld, const float* rope, int rope_rows, int n_q_heads, const void* q, int64_t q_ld,
+                       void* q_out, int64_t q_out_ld, int32_t* status, dflash_stream_t stream);
+
+/* The values that the cache holds for the batch's rows (slots lens[s] + j):
+ * k, v = device bf16 [rows][n_kv_heads][head_dim] out, strides as above. */
+int dflash_page_read(const dflash_pages* pages, const dflash_rows* rows, void* k, int64_t k_ld, void* v, int64_t v_ld,
+                     int32_t* status, dflash_stream_t stream);
+
+/* Attention of the batch's rows over the cache, their own slots included
+ * (append them first): for every row and query head
+ *   out = sum_c softmax_c(scale * <q, k_c>) v_c
+ * over the slots c that the row sees; zeros where it sees none. Query heads
+ * h * G .. h * G + G - 1 (G = n_q_heads / n_kv_heads, at most
+ * DFLASH_MAX_PAGE_GROUP) read kv head h.
+ * A row of stream s, the j-th, sees
+ *   - committed slots c < lens[s], and
+ *   - of the batch's slots lens[s] + m: CAUSAL: m <= j; BLOCK: all of its
+ *     stream; TREE: those with bit m set in the row's mask words (mask: device
+ *     uint32 [rows][mask_ld], mask_ld * 32 >= max_rows; dflash_tree_build's
+ *     node_mask);
+ * and with window > 0 of these only the slots whose position is less than
+ * `window` before the row's own or that are among the stream's first `sinks`
+ * slots. (A committed slot's position is its index. window 0: no limit, sinks
+ * without meaning.) Slots that no row of a stream sees are not used whatever
+ * they hold, and pages of such slots are not looked up beyond whole groups of
+ * 16 slots; a value some row sees has to be finite for the others' sake: a
+ * row's weight of zero times an infinity or NaN is NaN.
+ *   q, out: device bf16 [rows][n_q_heads][head_dim], rows q_ld / out_ld
+ *     elements apart (multiples of 8), 16-byte aligned.
+ *   scale > 0, finite.
+ * Scores, softmax and output sums are fp32; the softmax weights enter the
+ * second product rounded to bf16 (FP4 pages: to fp16, beside values exact in
+ * fp16), the output is rounded once. The sums' order depends on the batch's
+ * lengths. ws: 16-byte aligned, >= dflash_page_attention_workspace_bytes for
+ * the same pages, rows and heads; its content need not be kept or cleared,
+ * but two calls that overlap on the GPU must not share it. */
+enum { DFLASH_MASK_CAUSAL = 0, DFLASH_MASK_BLOCK = 1, DFLASH_MASK_TREE = 2 };
+int dflash_page_attention_workspace_bytes(const dflash_pages* pages, const dflash_rows* rows, int n_q_heads,
+                                          size_t* bytes);
+int dflash_page_attention(const dflash_pages* pages, const dflash_rows* rows, int n_q_heads, const void* q,
+                          int64_t q_ld, float scale, int window, int sinks, int mask_mode, const uint32_t* mask,
+                          int mask_ld, void* out, int64_t out_ld, int32_t* status, void* ws, size_t ws_bytes,
+                          dflash_stream_t stream);
+
+/* ---------------------------------------------------------------- logit rules
+ * What a request asks of the target's scores before they are verified:
+ * penalties for repeated tokens, biases, a grammar's mask. Run on the target's
+ * rows (and on the drafter's, where both sides sample) before dflash_verify or
+ * dflash_tree_verify.
+ *
+ * counts: device uint16 [streams][vocab], 16-byte aligned: bit 15 of an entry
+ * says that the token is in the stream's prompt, bits 0..14 how often it is in
+ * its output so far (at most 32767). The caller clears it for a new stream.
+ * dflash_token_counts adds tokens: `total` device int32 ids, stream s's at
+ * row_start[s] .. row_start[s + 1] - 1 (device int32 [streams + 1]) or, with
+ * row_start NULL, per_stream a stream (dflash_verify's out_tokens with
+ * per_stream 16: ids outside [0, vocab), its -1s among them, are skipped).
+ * prompt 1: marks them as prompt; 0: counts them as output. vocab a multiple
+ * of 8, total at most 2^38. */
+int dflash_token_counts(int streams, int vocab, void* counts, const int32_t* tokens, const int32_t* row_start,
+                        int per_stream, int64_t total, int prompt, dflash_stream_t stream);
+
+/* logits, out: device bf16 [streams][rows][vocab] (out may be logits), 16-byte
+ * aligned, rows at most DFLASH_MAX_TREE_NODES. For row n and token v, with c
+ * and p the stream's count and prompt bit of v and e the number of nodes m >=
+ * 1 on row n's path with tokens[m] == v,
+ *   x = logits; if p or c + e > 0: x = x > 0 ? x / repetition : x * repetition
+ *   if c + e > 0: x = (x - frequency * (c + e)) - presence
+ *   x = x + (the sum of v's biases)
+ *   x = -inf where the grammar's bit of v is 0
+ * in fp32, rounded once to bf16. Every part may be left out with a NULL:
+ *   counts           as above; needed by tokens and the penalties.
+ *   tokens           device int32 [streams][rows]: the draft's nodes (node 0,
+ *                    the anchor, is committed and so in the counts already).
+ *   node_mask        device uint32 [streams][rows][mask_ld], mask_ld * 32 >=
+ *                    rows: bit m of row n: node m is on row n's path (as
+ *                    dflash_tree_build writes it). NULL: a chain (m <= n).
+ *   repetition, frequency, presence
+ *                    device fp32 [streams] (NULL: 1, 0, 0), repetition > 0.
+ *   bias_start, bias_ids, bias_vals
+ *                    device int32 [streams + 1], int32 [n_bias], fp32
+ *                    [n_bias]: stream s's biases; ids in any order, equal ids
+ *                    add up in list order, ids outside [0, vocab) are skipped.
+ *   grammar          device uint32 [streams][rows][ceil(vocab / 32)]: bit v %
+ *                    32 of word v / 32 allows token v. */
+typedef struct dflash_rules {
+  const void* counts;
+  const int32_t* tokens;
+  const uint32_t* node_mask;
+  int32_t mask_ld;
+  int32_t n_bias;
+  const float *repetition, *frequency, *presence;
+  const int32_t *bias_start, *bias_ids;
+  const float* bias_vals;
+  const uint32_t* grammar;
+} dflash_rules;
+int dflash_logit_rules(int streams, int rows, int vocab, const void* logits, const dflash_rules* rules, void* out,
+                       dflash_stream_t stream);
 
 /* ---------------------------------------------------------------- verify
  * Target verification of S drafted blocks [EXPL 四; PROT "What is portable"].
