@@ -666,11 +666,19 @@ PagePlan page_attention_plan(const dflash_pages& c, const dflash_rows& r, int nq
   const int G = nq / c.n_kv_heads;
   const bool fp4 = c.format == DFLASH_PAGES_FP4;
   PagePlan p{};
-  p.tc = false;
-  p.tile = kTileRows;
-  p.unit = fp4 ? 32 : 16;
-  p.target = 152 * (fp4 ? 2 : 1);
-  p.min_units = 2 * kWarps;
+  const int64_t R = static_cast<int64_t>(r.max_rows) * G;
+  p.tc = c.head_dim >= 64 && R > kTileRows;
+  if (p.tc) {
+    p.tile = R > 512 ? 256 : 128;
+    p.unit = 128;
+    p.target = 152;
+    p.min_units = 4;
+  } else {
+    p.tile = kTileRows;
+    p.unit = fp4 ? 32 : 16;
+    p.target = 152 * (fp4 ? 2 : 1);
+    p.min_units = 2 * kWarps;
+  }
   const int64_t per_stream = (static_cast<int64_t>(r.max_rows) * G + p.tile - 1) / p.tile;
   const int64_t by_rows = (static_cast<int64_t>(r.rows) * G + p.tile - 1) / p.tile + c.streams;
   const int64_t tiles = std::min(c.streams * per_stream, by_rows);
@@ -690,7 +698,8 @@ int launch_page_attention(const PageAttnArgs& a, const PagePlan& p, bool fp4, cu
   int rc;
   {
     TraceScope ts(st, "page_attention", 0.0, 0.0);
-    if (D == 128) rc = fp4 ? launch_small<128, true>(a, p, st) : launch_small<128, false>(a, p, st);
+    if (p.tc) rc = launch_page_attention_tc(a, p, fp4, st);
+    else if (D == 128) rc = fp4 ? launch_small<128, true>(a, p, st) : launch_small<128, false>(a, p, st);
     else if (D == 64) rc = fp4 ? launch_small<64, true>(a, p, st) : launch_small<64, false>(a, p, st);
     else rc = fp4 ? launch_small<32, true>(a, p, st) : launch_small<32, false>(a, p, st);
   }

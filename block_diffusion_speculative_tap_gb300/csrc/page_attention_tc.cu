@@ -1,0 +1,810 @@
+// Attention over the paged target cache on the fifth-generation tensor cores
+// (tcgen05), for tiles of more than 16 (query row, head) pairs a kv head:
+// drafted blocks, draft trees, prompt chunks. Head dimension 64 or 128.
+//
+// A CTA runs two softmax streams, each with 128 rows, its own scores S, weights
+// P and output O in tensor memory (S and P share columns: 2 x 128 + 2 x D of
+// the 512). While one stream's four warps turn S into P, the tensor cores work
+// for the other:
+//   pair:   the streams are the halves of a 256-row tile; every K/V tile that
+//           lands in shared memory serves both (prompt chunks, where the
+//           tensor cores are the bound and L2 could not feed one tile each);
+//   parity: one 128-row tile, the streams take the even and the odd key tiles
+//           and are joined at the end (blocks and trees, where the cache's
+//           bytes are the bound).
+// One warp issues all MMAs in order: S_s(u+1) is issued behind P_s(u) V(u), so
+// the completion of scores also says that every earlier output product is
+// done, and a row's output may be rescaled then. The maximum in use moves only
+// when the true one passes it by 2^8, so rescaling is rare after a row's
+// first tiles.
+//
+// Keys come in tiles of 128 through a ring of slots, K and V alternating: bf16
+// pages by TMA, one box a page and 64 dims; 4-bit pages by four warps, a
+// thread a key: cp.async into a private staging row, codes and scales to fp16
+// in registers, 16-byte stores into the swizzled slot.
+//
+// V rows of slots that no row of the tile sees are zeroed in the slot (a
+// weight of zero must not meet what a stale slot holds). Every wait is
+// bounded.
+#include <cuda_fp16.h>
+
+#include "internal.h"
+#include "pages.h"
+#include "ptx.cuh"
+
+namespace dfl {
+
+namespace {
+
+constexpr int kTK = 128;                 // keys a tile
+constexpr int kMRows = 128;              // rows of a softmax stream
+constexpr float kRescale = 8.f;          // log2 by which the maximum in use may lag
+constexpr int kSoftThreads = 256;
+
+template <int D, bool FP4, bool PAIR>
+struct TcGeo {
+  static constexpr int kProd = FP4 ? 4 : 1;                 // producer warps
+  static constexpr int kThreads = kSoftThreads + 32 + 32 * kProd;
+  static constexpr int kSub = kTK * 128;                    // 128 rows x 64 dims
+  static constexpr int kSlot = kTK * D * 2;                 // a K or V tile
+  static constexpr int kQ = (PAIR ? 2 : 1) * kMRows * D * 2;
+  static constexpr int kRow = D / 2, kSc = D / 16;          // 4-bit row and scale bytes
+  static constexpr int kRaw = FP4 ? kTK * (kRow + 8) : 0;   // a staged 4-bit tile (scales padded to 8 bytes)
+  static constexpr int kStage = FP4 ? (PAIR ? 3 : 6) : 0;   // staged tiles
+  static constexpr int kSlots = D == 64 ? 8 : FP4 ? 4 : (PAIR ? 5 : 6);
+  static constexpr int kOffSlots = kQ;
+  static constexpr int kOffRaw = kOffSlots + kSlots * kSlot;
+  static constexpr int kOffBar = kOffRaw + kStage * kRaw;
+  static constexpr int kSmem = kOffBar + 512 + 1024;
+  static constexpr int kPartLd = D + 4;
+  static constexpr int kColO = 256;
+  static constexpr float kShift = FP4 ? 7.f : 0.f;  // P <= 2^(kRescale + kShift) in fp16
+  static_assert(kMRows * (kPartLd + 2) * 4 <= kSlots * kSlot, "the second stream's rows must fit the ring");
+  static_assert(kSmem <= 232448, "shared memory of an SM");
+};
+
+struct TcPageArgs {
+  CUtensorMap kmap, vmap;  // bf16: the pool's rows [n_pages * nkv * page][D], box {64, page}
+  PageAttnArgs a;
+};
+
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+// kind::f16 with fp16 (or bf16) A and B, fp32 accumulator; bit 16: B MN-major.
+constexpr uint32_t idesc16(bool half, int M, int N, bool b_mn) {
+  return (1u << 4) | (half ? 0u : (1u << 7) | (1u << 10)) | (b_mn ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void umma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <bool HALF>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if (HALF) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Eight 4-bit codes (low nibble first) to four fp16 pairs.
+__device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t e4m3x2(uint32_t two) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
+  return h;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t c;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+  return c;
+}
+
+// Bits i of the 32 slots from `base` on with lo <= base + i < hi.
+__device__ __forceinline__ uint32_t range_bits(int lo, int hi, int base) {
+  const int a = max(lo - base, 0), b = min(hi - base, 32);
+  if (b <= a) return 0u;
+  return (0xffffffffu >> (32 - b)) & (0xffffffffu << a);
+}
+
+template <int D, bool FP4, bool PAIR>
+__global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
+    page_attn_tc_kernel(const __grid_constant__ TcPageArgs P) {
+  using Ge = TcGeo<D, FP4, PAIR>;
+  constexpr int kSlots = Ge::kSlots;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const PageAttnArgs& a = P.a;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Ge::kOffBar);  // [kSlots] a tile is in its slot
+  uint64_t* empty = full + kSlots;   // [kSlots] the MMAs that read the slot are done
+  uint64_t* s_full = empty + kSlots; // [2] a stream's scores are in tensor memory
+  uint64_t* p_full = s_full + 2;     // [2] its weights are, and its output is rescaled
+  uint64_t* q_full = p_full + 2;     // the queries are in shared memory
+  uint64_t* o_full = q_full + 1;     // every MMA is done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 1);
+  int* abort_word = reinterpret_cast<int*>(tmem_slot + 1);
+  int* have_s = abort_word + 1;
+  Item* item_s = reinterpret_cast<Item*>(have_s + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = blockIdx.y;
+  int* err = a.r.status;
+
+  pdl_wait();
+  pdl_trigger();
+  if (warp == 0) {
+    Item it;
+    const bool have = find_item(a, static_cast<int>(blockIdx.x), false, &it);
+    if (lane == 0) {
+      *item_s = it;
+      *have_s = have;
+    }
+  }
+  if (threadIdx.x == 32) {
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&full[s], FP4 ? 32 * Ge::kProd : 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], kMRows);
+    }
+    mbar_init(q_full, PAIR ? 2 * kMRows : kMRows);
+    mbar_init(o_full, 1);
+    *abort_word = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  if (!*have_s) return;
+  const Item it = *item_s;
+  if (warp == 8) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  bool bad;
+  const StreamRows q = stream_rows(a.r, it.s, &bad);
+  // what the tile's rows see: from the window of the lowest position to the
+  // end of the last row's (positions of a tree are looked up)
+  const int64_t f0 = static_cast<int64_t>(it.tile) * a.tile;
+  const int j_lo = static_cast<int>(f0 / a.G);
+  const int j_hi = min(q.n - 1, static_cast<int>((f0 + a.tile - 1) / a.G));
+  int pos_lo = q.C + j_lo, pos_hi = q.C + j_hi;
+  if (a.r.depth && a.window > 0) {
+    pos_lo = 0x7fffffff;
+    pos_hi = 0;
+    for (int j = j_lo + lane; j <= j_hi; j += 32) {
+      const int p = row_pos(a.r, q, j);
+      pos_lo = min(pos_lo, p);
+      pos_hi = max(pos_hi, p);
+    }
+    pos_lo = __reduce_min_sync(0xffffffffu, pos_lo);
+    pos_hi = __reduce_max_sync(0xffffffffu, pos_hi);
+  }
+  const int hi = q.C + (a.mode == DFLASH_MASK_CAUSAL ? j_hi + 1 : q.n);
+  const int lo = a.window > 0 ? min(q.C, max(0, pos_lo - a.window + 1)) : 0;
+  const int lo_max = a.window > 0 ? max(0, pos_hi - a.window + 1) : 0;
+  const int sinks = min(a.sinks, hi);
+  const bool plain = a.mode != DFLASH_MASK_TREE && a.r.depth == nullptr;  // visibility is a range of slots
+  // slots below this are seen by every row as far as the rows' order goes
+  const int all_end = !plain ? q.C : a.mode == DFLASH_MASK_CAUSAL ? q.C + j_lo + 1 : q.C + q.n;
+  const UnitRange ur = unit_range(lo, hi, a.sinks, kTK);
+  const int i0 = static_cast<int>(static_cast<long long>(ur.n) * it.split / it.ns);
+  const int i1 = static_cast<int>(static_cast<long long>(ur.n) * (it.split + 1) / it.ns);
+  const int nt = i1 - i0;  // key tiles
+  auto slot0 = [&](int t) {
+    const int i = i0 + t;
+    return (i < ur.nsink ? i : ur.first + (i - ur.nsink)) * kTK;
+  };
+  // whether every slot of a tile is seen by some row (else its V is cleaned)
+  auto inside = [&](int kb) { return (kb >= lo && kb + kTK <= hi) || kb + kTK <= sinks; };
+  auto live = [&](int slot) { return (slot >= lo && slot < hi) || slot < sinks; };
+  auto page_of = [&](int slot) -> int {
+    const int col = slot >> a.c.page_log2;
+    const int p = col < a.c.cols ? a.c.table[static_cast<int64_t>(it.s) * a.c.cols + col] : -1;
+    return p >= 0 && p < a.c.n_pages ? p : -1;
+  };
+  // The ring's order: pair: K0 V0 K1 V1 ..; parity: K0 K1 V0 K2 V1 K3 ...
+  // Entry e: K (kv 0) or V (kv 1) of tile t.
+  const int entries = 2 * nt;
+  auto entry = [&](int e, int* kv, int* t) {
+    if (PAIR || nt < 2) {
+      *kv = e & 1;
+      *t = e >> 1;
+    } else if (e < 2) {
+      *kv = 0;
+      *t = e;
+    } else if (e == entries - 1) {
+      *kv = 1;
+      *t = nt - 1;
+    } else {
+      *kv = (e & 1) ? 0 : 1;
+      *t = (e & 1) ? (e + 1) >> 1 : (e - 2) >> 1;
+    }
+  };
+
+  if (warp == 8) {
+    // ------------------------------------------------ MMA issuer
+    constexpr uint32_t kIdS = idesc16(FP4, kMRows, kTK, false);
+    constexpr uint32_t kIdO = idesc16(FP4, kMRows, D, true);
+    bool ok = nt > 0 && mbar_wait(q_full, 0, err, DFLASH_STATUS_TIMEOUT, abort_word);
+    ok = __all_sync(0xffffffffu, ok);
+    bool any = false;
+    int e = 0;  // next ring entry
+    auto wait_entry = [&]() -> int {
+      const int sl = e % kSlots;
+      ok = ok && mbar_wait(&full[sl], (e / kSlots) & 1, err, DFLASH_STATUS_TIMEOUT, abort_word);
+      ok = __all_sync(0xffffffffu, ok);
+      ++e;
+      return sl;
+    };
+    auto scores = [&](int s, int sl) {
+      if (lane != 0) return;
+      tc_fence_after();
+      const uint32_t kb = sbase + Ge::kOffSlots + sl * Ge::kSlot;
+      const uint32_t qb = sbase + (PAIR ? s * kMRows * D * 2 : 0);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk >> 2) * Ge::kSub + (kk & 3) * 32;
+        umma_bf16(tmem + s * 128, sdesc_sw128(qb + off), sdesc_sw128(kb + off), kIdS, kk > 0 ? 1u : 0u);
+      }
+      any = true;
+      umma_commit(&s_full[s]);
+    };
+    auto output = [&](int s, int sl, bool first) {
+      if (lane != 0) return;
+      tc_fence_after();
+      const uint32_t vb = sbase + Ge::kOffSlots + sl * Ge::kSlot;
+#pragma unroll
+      for (int kk = 0; kk < kTK / 16; ++kk)
+        umma_ta(tmem + Ge::kColO + s * D, tmem + s * 128 + kk * 8, sdesc_mn(vb + kk * 16 * 128, Ge::kSub), kIdO,
+                (!first || kk > 0) ? 1u : 0u);
+    };
+    auto release = [&](int sl) {
+      if (lane == 0) umma_commit(&empty[sl]);
+    };
+    // V rows no row sees: whatever the slots hold, they count as zero (4-bit
+    // tiles are written clean)
+    auto clean = [&](int sl, int kb) {
+      if (FP4 || inside(kb)) return;
+      for (int r = 0; r < kTK; ++r) {
+        if (live(kb + r)) continue;
+        uint8_t* row = smem + Ge::kOffSlots + sl * Ge::kSlot + r * 128;
+        if (lane < D / 8)
+          *reinterpret_cast<uint4*>(row + (lane >> 3) * Ge::kSub + (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_async();
+      __syncwarp();
+    };
+    auto wait_p = [&](int s, int u) {
+      ok = ok && mbar_wait(&p_full[s], u & 1, err, DFLASH_STATUS_TIMEOUT, abort_word);
+      ok = __all_sync(0xffffffffu, ok);
+    };
+    if (PAIR) {
+      if (ok) {
+        const int sl = wait_entry();
+        if (ok) {
+          scores(0, sl);
+          scores(1, sl);
+          release(sl);
+        }
+      }
+      for (int t = 0; t < nt && ok; ++t) {
+        int vs = 0, ks = 0;
+        wait_p(0, t);
+        if (ok) vs = wait_entry();
+        if (!ok) break;
+        clean(vs, slot0(t));
+        output(0, vs, t == 0);
+        if (t + 1 < nt) {
+          ks = wait_entry();
+          if (!ok) break;
+          scores(0, ks);
+        }
+        wait_p(1, t);
+        if (!ok) break;
+        output(1, vs, t == 0);
+        release(vs);
+        if (t + 1 < nt) {
+          scores(1, ks);
+          release(ks);
+        }
+      }
+    } else {
+      for (int t = 0; t < 2 && t < nt && ok; ++t) {
+        if (nt < 2 && t > 0) break;
+        const int sl = wait_entry();
+        if (!ok) break;
+        scores(t, sl);
+        release(sl);
+      }
+      for (int t = 0; t < nt && ok; ++t) {
+        const int s = t & 1;
+        wait_p(s, t >> 1);
+        if (!ok) break;
+        const int vs = wait_entry();
+        if (!ok) break;
+        clean(vs, slot0(t));
+        output(s, vs, t < 2);
+        release(vs);
+        if (t + 2 < nt) {
+          const int ks = wait_entry();
+          if (!ok) break;
+          scores(s, ks);
+          release(ks);
+        }
+      }
+    }
+    // every MMA completes before tensor memory is read for the last time or released
+    if (lane == 0 && any) {
+      umma_commit(o_full);
+      mbar_wait(o_full, 0, err, DFLASH_STATUS_TIMEOUT, nullptr);
+    }
+    __syncwarp();
+  } else if (warp > 8 && !FP4) {
+    // ------------------------------------------------ TMA producer: a lane a box
+    const int boxes = kTK / a.c.page;  // boxes of 64 dims a tile: boxes * D / 64 <= 16
+    int issued = 0;
+    for (int e = 0; e < entries; ++e) {
+      const int sl = e % kSlots;
+      bool ok = e < kSlots || mbar_wait(&empty[sl], ((e / kSlots) & 1) ^ 1u, err, DFLASH_STATUS_TIMEOUT, abort_word);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      int kv, t;
+      entry(e, &kv, &t);
+      const int kb = slot0(t);
+      const int b = lane % boxes, half = lane / boxes;
+      const int slot = kb + b * a.c.page;
+      const bool need = half < D / 64 && ((slot < hi && slot + a.c.page > lo) || slot < sinks);
+      const int pg = need ? page_of(slot) : -1;
+      if (need && pg < 0) flag_status(err, DFLASH_STATUS_BAD_PAGE);
+      const unsigned go = __ballot_sync(0xffffffffu, pg >= 0);
+      if (lane == 0) mbar_arrive_expect_tx(&full[sl], __popc(go) * a.c.page * 128);
+      __syncwarp();
+      if (pg >= 0)
+        tma_tile(sbase + Ge::kOffSlots + sl * Ge::kSlot + half * Ge::kSub + b * a.c.page * 128,
+                 kv ? &P.vmap : &P.kmap, &full[sl], half * 64, (pg * a.c.nkv + h) * a.c.page);
+      issued = e + 1;
+    }
+    // no copy may still be landing when the slots are used again below
+    for (int e = max(0, issued - kSlots); e < issued; ++e)
+      mbar_wait(&full[e % kSlots], (e / kSlots) & 1, err, DFLASH_STATUS_TIMEOUT, nullptr);
+  } else if (FP4 && warp > 8) {
+    // ------------------------------------------------ 4-bit producers: a thread a key
+    if constexpr (FP4) {
+    constexpr int kSt = Ge::kStage;
+    const int key = threadIdx.x - (kSoftThreads + 32);
+    const uint32_t raw_u = sbase + Ge::kOffRaw + key * Ge::kRow;
+    const uint8_t* raw = smem + Ge::kOffRaw + key * Ge::kRow;
+    constexpr int kPieces = Ge::kRow / 16;
+    auto swp = [&](int c) { return kPieces == 4 ? c ^ ((key >> 1) & 3) : c ^ ((key >> 2) & 1); };
+    uint32_t have = 0;  // staged tiles in flight, newest in bit 0: this thread's key is there
+    auto stage = [&](int e) {
+      have <<= 1;
+      if (e < entries) {
+        int kv, t;
+        entry(e, &kv, &t);
+        const int slot = slot0(t) + key;
+        const int pg = live(slot) ? page_of(slot) : -1;
+        if (pg >= 0) {
+          have |= 1u;
+          const int64_t row = (static_cast<int64_t>(pg) * a.c.nkv + h) * a.c.page + (slot & (a.c.page - 1));
+          const uint8_t* src = (kv ? a.c.v : a.c.k) + row * Ge::kRow;
+          const uint8_t* ssc = (kv ? a.c.vs : a.c.ks) + row * Ge::kSc;
+          const uint32_t d0 = raw_u + (e % kSt) * Ge::kRaw;
+#pragma unroll
+          for (int c = 0; c < kPieces; ++c)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d0 + swp(c) * 16), "l"(src + c * 16)
+                         : "memory");
+          const uint32_t ds = sbase + Ge::kOffRaw + (e % kSt) * Ge::kRaw + kTK * Ge::kRow + key * 8;
+          if (Ge::kSc == 8)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(ds), "l"(ssc) : "memory");
+          else
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ds), "l"(ssc) : "memory");
+        } else if (live(slot)) {
+          flag_status(err, DFLASH_STATUS_BAD_PAGE);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int e = 0; e + 1 < kSt; ++e) stage(e);
+    for (int e = 0; e < entries; ++e) {
+      stage(e + kSt - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kSt - 1) : "memory");
+      const int sl = e % kSlots;
+      const bool ok =
+          e < kSlots || mbar_wait(&empty[sl], ((e / kSlots) & 1) ^ 1u, err, DFLASH_STATUS_TIMEOUT, abort_word);
+      if (!ok) break;
+      const bool there = (have >> (kSt - 1)) & 1u;
+      const uint8_t* src = raw + (e % kSt) * Ge::kRaw;
+      const uint32_t* scp =
+          reinterpret_cast<const uint32_t*>(smem + Ge::kOffRaw + (e % kSt) * Ge::kRaw + kTK * Ge::kRow + key * 8);
+      uint32_t sw[2] = {0u, 0u};  // a key that is not there: all its values are zero
+      if (there) {
+        sw[0] = scp[0];
+        if (Ge::kSc == 8) sw[1] = scp[1];
+      }
+      uint8_t* dst = smem + Ge::kOffSlots + sl * Ge::kSlot + key * 128;
+#pragma unroll
+      for (int c = 0; c < kPieces; ++c) {
+        const uint4 w4 = there ? *reinterpret_cast<const uint4*>(src + swp(c) * 16) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+        const uint32_t sc2 = e4m3x2((sw[c >> 1] >> (16 * (c & 1))) & 0xffffu);  // scales of groups 2c, 2c + 1
+        const uint32_t g2[2] = {__byte_perm(sc2, 0, 0x1010), __byte_perm(sc2, 0, 0x3232)};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          uint32_t f[4];
+          e2m1x8(w[x], f);
+          const uint32_t gs = g2[x >> 1];
+          const int d8 = c * 4 + x;  // 8 dims: 16 bytes of the slot's row
+          *reinterpret_cast<uint4*>(dst + (d8 >> 3) * Ge::kSub + (((d8 & 7) ^ (key & 7)) << 4)) =
+              make_uint4(hmul2(f[0], gs), hmul2(f[1], gs), hmul2(f[2], gs), hmul2(f[3], gs));
+        }
+      }
+      fence_async();
+      mbar_arrive(&full[sl]);
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+  } else {
+    // ------------------------------------------------ softmax streams
+    const int s = warp >> 2, q4 = warp & 3;
+    const int r = q4 * 32 + lane;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
+    const uint32_t ts = tl + s * 128, to = tl + Ge::kColO + s * D;
+    const int64_t f = f0 + (PAIR ? s * kMRows : 0) + r;
+    RowView rv;
+    const int jr = static_cast<int>(f / a.G);
+    const int hd = static_cast<int>(f - static_cast<int64_t>(jr) * a.G);
+    rv.j = jr < q.n ? jr : -1;
+    rv.pos = rv.j >= 0 ? row_pos(a.r, q, jr) : 0;
+    rv.back = a.window > 0 ? max(0, rv.pos - a.window + 1) : 0;
+    const bool idle = __all_sync(0xffffffffu, rv.j < 0);  // a warp of padding rows takes no part
+    float sc = a.scale;
+    if (PAIR || s == 0) {
+      // this thread's query row, swizzled as TMA would write it
+      const __nv_bfloat16* src =
+          rv.j >= 0 ? a.q + static_cast<int64_t>(q.row0 + jr) * a.q_ld + (h * a.G + hd) * D : nullptr;
+      uint8_t* dst = smem + (PAIR ? s * kMRows * D * 2 : 0) + r * 128;
+      float down = 1.f;
+      if (FP4) {
+        float top = 0.f;
+        if (src)
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 w = reinterpret_cast<const uint4*>(src)[c];
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[x] << 16)), fabsf(__uint_as_float(u[x] & 0xffff0000u))));
+          }
+        const int ex = (top > 0.f && top < INFINITY) ? max(-100, min(126, ilogbf(top))) : 0;
+        down = ldexpf(1.f, -ex);
+        sc *= ldexpf(1.f, ex);
+      }
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        uint4 w = src ? reinterpret_cast<const uint4*>(src)[c] : make_uint4(0u, 0u, 0u, 0u);
+        if (FP4) {
+          uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            u[x] = pack2<true>(__uint_as_float(u[x] << 16) * down, __uint_as_float(u[x] & 0xffff0000u) * down);
+          w = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+        *reinterpret_cast<uint4*>(dst + (c >> 3) * Ge::kSub + (((c & 7) ^ (r & 7)) << 4)) = w;
+      }
+      fence_async();
+      mbar_arrive(q_full);
+    }
+    if (FP4 && !PAIR) {
+      // both streams scale a row's scores alike
+      float* scs = reinterpret_cast<float*>(smem + Ge::kOffBar + 512);
+      if (s == 0) scs[r] = sc;
+      named_bar_sync(1, kSoftThreads);
+      sc = scs[r];
+    }
+    float m = -INFINITY, l = 0.f;
+    const int n_mine = PAIR ? nt : (nt + 1 - s) / 2;
+    bool ok = true;
+    for (int u = 0; u < n_mine; ++u) {
+      ok = mbar_wait(&s_full[s], u & 1, err, DFLASH_STATUS_TIMEOUT, abort_word);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (idle) {
+        mbar_arrive(&p_full[s]);
+        continue;
+      }
+      tc_fence_after();
+      const int kb = slot0(PAIR ? u : 2 * u + s);
+      const bool whole = kb + kTK <= all_end && (kb >= lo_max || kb + kTK <= sinks);
+      uint32_t vis[4];
+      if (!whole) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const int base = kb + 32 * w;
+          uint32_t b;
+          if (plain) {
+            const int end = a.mode == DFLASH_MASK_CAUSAL ? q.C + rv.j + 1 : q.C + q.n;
+            b = range_bits(rv.back, end, base) | range_bits(0, min(a.sinks, end), base);
+          } else {
+            b = range_bits(rv.back, q.C, base) | range_bits(0, min(a.sinks, q.C), base);
+            const uint32_t blk = range_bits(q.C, q.C + q.n, base);
+            if (blk && rv.j >= 0) {
+              if (a.window == 0 || rv.pos - q.C < a.window) {
+                if (a.mode == DFLASH_MASK_TREE) {
+                  const uint32_t* mw = a.mask + static_cast<int64_t>(q.row0 + rv.j) * a.mask_ld;
+                  const int m0 = base - q.C, w0 = m0 >> 5, nw = (q.n + 31) >> 5;
+                  const uint32_t x0 = w0 >= 0 && w0 < nw ? mw[w0] : 0u;
+                  const uint32_t x1 = w0 + 1 >= 0 && w0 + 1 < nw ? mw[w0 + 1] : 0u;
+                  b |= blk & __funnelshift_r(x0, x1, m0 & 31);
+                } else {
+                  b |= a.mode == DFLASH_MASK_CAUSAL ? blk & range_bits(q.C, q.C + rv.j + 1, base) : blk;
+                }
+              } else {
+                for (int i = 0; i < 32; ++i)
+                  if (((blk >> i) & 1u) && sees(a, q, rv, base + i)) b |= 1u << i;
+              }
+            }
+          }
+          vis[w] = rv.j >= 0 ? b : 0u;
+        }
+      }
+      // the row's largest score of the tile; 64 scores at a time, read again
+      // for the weights (128 held across would spill)
+      float sv[64];
+      auto load_scores = [&](int c) {
+        tmem_ld32(ts + c * 64, reinterpret_cast<uint32_t*>(sv));
+        tmem_ld32(ts + c * 64 + 32, reinterpret_cast<uint32_t*>(sv) + 32);
+        tmem_wait_ld();
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (!((vis[c * 2 + (i >> 5)] >> (i & 31)) & 1u)) sv[i] = -INFINITY;
+        }
+      };
+      float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        load_scores(c);
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) {
+          t0 = fmaxf(t0, sv[i]);
+          t1 = fmaxf(t1, sv[i + 1]);
+          t2 = fmaxf(t2, sv[i + 2]);
+          t3 = fmaxf(t3, sv[i + 3]);
+        }
+      }
+      const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * sc;
+      // The scores are complete, so every output product before them is too:
+      // the output may be rescaled in place.
+      const bool need = top > m + kRescale;
+      if (__any_sync(0xffffffffu, need)) {
+        const float alpha = !need ? 1.f : (m == -INFINITY ? 0.f : ex2f(m - top));
+        l *= alpha;
+        if (u > 0) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            float v[32];
+            tmem_ld32(to + c * 32, reinterpret_cast<uint32_t*>(v));
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] *= alpha;
+            tmem_st32(to + c * 32, reinterpret_cast<uint32_t*>(v));
+          }
+        }
+        if (need) m = top;
+      }
+      const float neg = m == -INFINITY ? 0.f : Ge::kShift - m;
+      float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t pk[32];  // columns 32c ..: scores read already
+        load_scores(c);
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) {
+          float* x = sv + i;
+          x[0] = ex2f(fmaf(x[0], sc, neg));
+          x[1] = ex2f(fmaf(x[1], sc, neg));
+          x[2] = ex2f(fmaf(x[2], sc, neg));
+          x[3] = ex2f(fmaf(x[3], sc, neg));
+          a0 += x[0];
+          a1 += x[1];
+          a2 += x[2];
+          a3 += x[3];
+          pk[i / 2] = pack2<FP4>(x[0], x[1]);
+          pk[i / 2 + 1] = pack2<FP4>(x[2], x[3]);
+        }
+        tmem_st32(ts + c * 32, pk);
+      }
+      l += (a0 + a1) + (a2 + a3);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&p_full[s]);
+    }
+    // ------------------------------------------------ output
+    if (nt > 0) {
+      ok = ok && mbar_wait(o_full, 0, err, DFLASH_STATUS_TIMEOUT, abort_word);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+    }
+    const bool mine = ok && n_mine > 0 && !idle;
+    float* xo = reinterpret_cast<float*>(smem + Ge::kOffSlots);  // [128][kPartLd] the second stream's rows
+    float* xm = xo + kMRows * Ge::kPartLd;                       // [128][2]
+    float m1 = -INFINITY, l1 = 0.f;
+    if (!PAIR) {
+      if (s == 1) {
+        xm[2 * r] = mine ? m : -INFINITY;
+        xm[2 * r + 1] = mine ? l : 0.f;
+        if (mine) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            float v[32];
+            tmem_ld32(to + c * 32, reinterpret_cast<uint32_t*>(v));
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<float4*>(xo + r * Ge::kPartLd + c * 32 + i) =
+                  make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          }
+        }
+      }
+      named_bar_sync(1, kSoftThreads);
+      if (s == 0) {
+        m1 = xm[2 * r];
+        l1 = xm[2 * r + 1];
+      }
+    }
+    if ((PAIR || s == 0) && !idle) {
+      const float M = fmaxf(mine ? m : -INFINITY, m1);
+      const float w0 = mine && m != -INFINITY ? ex2f(m - M) : 0.f;
+      const float w1 = m1 != -INFINITY ? ex2f(m1 - M) : 0.f;
+      const float den = (w0 > 0.f ? w0 * l : 0.f) + (w1 > 0.f ? w1 * l1 : 0.f);
+      const bool split = it.ns > 1;
+      const float inv = split ? 1.f : M == -INFINITY ? 0.f : 1.f / den;
+      const bool write = rv.j >= 0 && (!split || it.slot < a.slots);
+      const int64_t prow = (static_cast<int64_t>(it.slot) * a.c.nkv + h) * a.tile + (PAIR ? s * kMRows : 0) + r;
+      __nv_bfloat16* dst = a.out + static_cast<int64_t>(q.row0 + jr) * a.out_ld + (h * a.G + hd) * D;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        float v[32];
+        if (mine) {
+          tmem_ld32(to + c * 32, reinterpret_cast<uint32_t*>(v));
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = w0 > 0.f ? v[i] * w0 : 0.f;
+        if (!PAIR && w1 > 0.f) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(xo + r * Ge::kPartLd + c * 32 + i);
+            v[i] = fmaf(x.x, w1, v[i]);
+            v[i + 1] = fmaf(x.y, w1, v[i + 1]);
+            v[i + 2] = fmaf(x.z, w1, v[i + 2]);
+            v[i + 3] = fmaf(x.w, w1, v[i + 3]);
+          }
+        }
+        if (!write) continue;
+        if (split) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(a.part_o + prow * D + c * 32 + i) =
+                make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+            *reinterpret_cast<uint4*>(dst + c * 32 + i) =
+                make_uint4(pack2<false>(v[i] * inv, v[i + 1] * inv), pack2<false>(v[i + 2] * inv, v[i + 3] * inv),
+                           pack2<false>(v[i + 4] * inv, v[i + 5] * inv), pack2<false>(v[i + 6] * inv, v[i + 7] * inv));
+        }
+      }
+      if (split && write) *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(M, den);
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+template <int D, bool FP4, bool PAIR>
+int launch(const TcPageArgs& P, const PagePlan& p, cudaStream_t st) {
+  using Ge = TcGeo<D, FP4, PAIR>;
+  auto kern = page_attn_tc_kernel<D, FP4, PAIR>;
+  constexpr int kBytes = Ge::kSmem + (FP4 && !PAIR ? 512 : 0);
+  static_assert(kBytes <= 232448, "shared memory of an SM");
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) != cudaSuccess) {
+    cudaGetLastError();
+    return DFLASH_E_CUDA;
+  }
+  const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(p.items), static_cast<unsigned>(P.a.c.nkv)),
+                                   dim3(Ge::kThreads), kBytes, st, P);
+  count_launch();
+  return cuda_status(e);
+}
+
+}  // namespace
+
+int launch_page_attention_tc(const PageAttnArgs& a, const PagePlan& p, bool fp4, cudaStream_t st) {
+  TcPageArgs P;
+  P.a = a;
+  const bool pair = p.tile == 2 * kMRows;
+  if (fp4) {
+    if (a.c.d == 128) return pair ? launch<128, true, true>(P, p, st) : launch<128, true, false>(P, p, st);
+    return pair ? launch<64, true, true>(P, p, st) : launch<64, true, false>(P, p, st);
+  }
+  const int64_t rows = static_cast<int64_t>(a.c.n_pages) * a.c.nkv * a.c.page;
+  int rc = encode_kmajor_map(&P.kmap, a.c.k, rows, a.c.d, a.c.d, a.c.page);
+  if (!rc) rc = encode_kmajor_map(&P.vmap, a.c.v, rows, a.c.d, a.c.d, a.c.page);
+  if (rc) return rc;
+  if (a.c.d == 128) return pair ? launch<128, false, true>(P, p, st) : launch<128, false, false>(P, p, st);
+  return pair ? launch<64, false, true>(P, p, st) : launch<64, false, false>(P, p, st);
+}
+
+}  // namespace dfl

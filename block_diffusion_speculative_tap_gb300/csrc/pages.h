@@ -142,12 +142,13 @@ __device__ __forceinline__ bool find_item(const PageAttnArgs& a, int want, bool 
       const int before = base + __shfl_sync(0xffffffffu, ic - cnt, l);
       const int nsl = __shfl_sync(0xffffffffu, ns, l);
       const int slot0 = slots + __shfl_sync(0xffffffffu, ip - part, l);
-      const int rel = want - before;
+      const int rel = want - before, tiles = __shfl_sync(0xffffffffu, mt, l);
+      const int tile = split_only ? rel : rel / nsl;
       out->s = s0 + l;
       out->ns = nsl;
-      out->tile = split_only ? rel : rel / nsl;
-      out->split = split_only ? 0 : rel - out->tile * nsl;
-      out->slot = slot0 + out->tile * nsl + out->split;
+      out->tile = tiles - 1 - tile;  // the last rows see most: their items start first
+      out->split = split_only ? 0 : rel - tile * nsl;
+      out->slot = slot0 + tile * nsl + out->split;
       return true;
     }
     base += __shfl_sync(0xffffffffu, ic, 31);
@@ -194,5 +195,6 @@ struct PagePlan {
 };
 PagePlan page_attention_plan(const dflash_pages& c, const dflash_rows& r, int nq);
 int launch_page_attention(const PageAttnArgs& a, const PagePlan& p, bool fp4, cudaStream_t st);
+int launch_page_attention_tc(const PageAttnArgs& a, const PagePlan& p, bool fp4, cudaStream_t st);
 
 }  // namespace dfl
