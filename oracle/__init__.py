@@ -11,3 +11,4 @@ even) at exactly the tensors the drafter stores or feeds to a matrix product.
 See ``oracle.dflash`` for the functions and the passages each one follows.
 """
 from .dflash import *  # noqa: F401,F403
+from .target import *  # noqa: F401,F403
