@@ -5,25 +5,29 @@
 //   out_r = sum_c softmax_c(scale * q_r . k_c) v_c  over the slots c row r sees
 //
 // in one pass over the keys: a running maximum m (log2 domain), sum l and
-// output O in fp32, rescaled when the maximum moves. One tile of 16 rows is
-// the M side of m16n8k16 MMAs; its G heads share every K/V byte.
+// output O in fp32, rescaled when the maximum moves. The products are taken
+// transposed, S^T = K Q^T and O^T = V^T P^T, on m16n8k16 MMAs: 16 keys (16
+// dims) on M and one or two blocks of 8 rows on N, so a token of up to 8 heads
+// a kv head wastes no rows and the heads share every K/V byte.
 //
-// A CTA's warps take the units (kKeys slots) of the CTA's slice in turn, each
+// A CTA's warps take the units (kKeys slots) of a segment in turn, each
 // through its own ring of cp.async stages, so no barrier stands inside the
-// loop. The order of the dims inside a dot product and of the output columns
-// over the MMA's n-tiles is free; it is chosen so that each lane's fragments
-// are whole 16-byte pieces of the rows as they lie in the cache (K: dims of
-// piece 4c + t of key g; V: the keys 2t, 2t+1, 2t+8, 2t+9 at piece g, pairs
-// of keys joined by byte permutes) and 4-bit codes become fp16 pairs in
+// loop. The order of the dims inside a dot product and of the output's dims
+// over the MMAs is free; it is chosen so that each lane's fragments are whole
+// 16-byte pieces of the rows as they lie in the cache (K: dims of piece 4c + t
+// of keys g and g + 8; V: the keys 2t, 2t+1, 2t+8, 2t+9 at piece g, pairs of
+// keys joined by byte permutes) and 4-bit codes become fp16 pairs in
 // registers, with no pass through shared memory in between. 4-bit values
 // (e2m1 times e4m3) are exact in fp16; queries go to fp16 over a power of two
 // a row, so they neither overflow nor lose more than fp32's own rounding of
 // the largest element (2^-25 of it).
 //
-// Few rows and long caches: the slots of a stream are cut into slices of
-// about equal length over all streams (find_item), a slice's (m, l, O) goes
-// to the workspace and page_combine_kernel joins a row's slices.
+// Few rows and long caches: CTAs take equal shares of all streams' keys (see
+// Share), a part's (m, l, O) goes to the workspace and page_combine_kernel
+// joins a row's parts.
 #include <cuda_fp16.h>
+
+#include <algorithm>
 
 #include "internal.h"
 #include "pages.h"
@@ -33,23 +37,23 @@ namespace dfl {
 
 namespace {
 
-constexpr int kTileRows = 16;
 constexpr int kWarps = 8;
 
-template <int D, bool FP4>
+template <int D, bool FP4, int NB>
 struct Geo {
   static constexpr int kRow = FP4 ? D / 2 : 2 * D;  // bytes of a key's codes or values
   static constexpr int kSc = FP4 ? D / 16 : 0;      // scale bytes a key
   static constexpr int kKeys = FP4 ? 32 : 16;       // keys a unit
   static constexpr int kSub = kKeys / 16;
   static constexpr int kStages = 3;
+  static constexpr int kTile = 8 * NB;
   static constexpr int kOffV = kKeys * kRow;
   static constexpr int kOffKs = 2 * kKeys * kRow;
   static constexpr int kOffVs = kOffKs + kKeys * kSc;
   static constexpr int kStage = 2 * kKeys * (kRow + kSc);
   static constexpr int kPartLd = D + 4;
   static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kMerge = kWarps * kTileRows * (kPartLd + 2) * 4;
+  static constexpr int kMerge = kWarps * kTile * (kPartLd + 2) * 4;
   static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
   static constexpr float kShift = FP4 ? 8.f : 0.f;  // log2 of the factor P carries into fp16
 };
@@ -124,47 +128,54 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi, bool half) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <int D, bool FP4>
+// An 8x8 matrix of 16-bit values, a row a four lanes, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+template <int D, bool FP4, int NB>
 __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(const __grid_constant__ PageAttnArgs a) {
-  using G_ = Geo<D, FP4>;
-  constexpr int kKeys = G_::kKeys, kRow = G_::kRow, kSub = G_::kSub, kNT = D / 8, kST = G_::kStages;
+  using G_ = Geo<D, FP4, NB>;
+  constexpr int kKeys = G_::kKeys, kRow = G_::kRow, kSub = G_::kSub, kMT = D / 16, kST = G_::kStages;
+  constexpr int kTile = G_::kTile;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ Item item_s;
-  __shared__ int have_s;
+  __shared__ Run run;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int h = blockIdx.y;
   pdl_wait();
   pdl_trigger();
-  if (warp == 0) {
-    Item it;
-    const bool have = find_item(a, static_cast<int>(blockIdx.x), false, &it);
-    if (lane == 0) {
-      item_s = it;
-      have_s = have;
-    }
-  }
+  if (warp == 0) run_begin(a, &run);
+  for (bool first = true;; first = false) {
+  if (warp == 0) run_next(a, &run);
   __syncthreads();
-  if (!have_s) return;
-  const Item it = item_s;
+  if (!run.left) return;
+  const Segment sg = run.seg;
+  const int h = sg.h;
+  const bool part = sg.x0 > 0 || sg.x1 < sg.u;
+  const int64_t part_row = (2ll * blockIdx.x + (first ? 0 : 1)) * kTile;
   bool bad;
-  const StreamRows q = stream_rows(a.r, it.s, &bad);
+  const StreamRows q = stream_rows(a.r, sg.s, &bad);
 
-  // this thread's two rows, and what the tile's rows see
-  RowView rv[2];
+  // this lane's rows 8b + 2t, 8b + 2t + 1 of the scores, and what the tile's rows see
+  RowView rv[NB][2];
   int lo = 0x7fffffff, lo_max = -1, j_max = 0;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t f = static_cast<int64_t>(it.tile) * kTileRows + g + 8 * i;
-    const int j = static_cast<int>(f / a.G);
-    rv[i].j = j < q.n ? j : -1;
-    rv[i].pos = rv[i].j >= 0 ? row_pos(a.r, q, j) : 0;
-    rv[i].back = a.window > 0 ? max(0, rv[i].pos - a.window + 1) : 0;
-    if (rv[i].j >= 0) {
-      lo = min(lo, rv[i].back);
-      lo_max = max(lo_max, rv[i].back);
-      j_max = max(j_max, j);
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t f = static_cast<int64_t>(sg.tile) * kTile + 8 * b + 2 * t + i;
+      const int j = static_cast<int>(f / a.G);
+      RowView& v = rv[b][i];
+      v.j = j < q.n ? j : -1;
+      v.pos = v.j >= 0 ? row_pos(a.r, q, j) : 0;
+      v.back = a.window > 0 ? max(0, v.pos - a.window + 1) : 0;
+      if (v.j >= 0) {
+        lo = min(lo, v.back);
+        lo_max = max(lo_max, v.back);
+        j_max = max(j_max, j);
+      }
     }
-  }
   lo = __reduce_min_sync(0xffffffffu, lo);
   lo_max = __reduce_max_sync(0xffffffffu, lo_max);
   j_max = __reduce_max_sync(0xffffffffu, j_max);
@@ -172,74 +183,10 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
   lo = min(lo, q.C);
   const int sinks = min(a.sinks, hi);
   const UnitRange ur = unit_range(lo, hi, a.sinks, kKeys);
-  const int i0 = static_cast<int>(static_cast<long long>(ur.n) * it.split / it.ns);
-  const int i1 = static_cast<int>(static_cast<long long>(ur.n) * (it.split + 1) / it.ns);
+  const int i0 = static_cast<int>(static_cast<long long>(ur.n) * sg.x0 / sg.u);
+  const int i1 = static_cast<int>(static_cast<long long>(ur.n) * sg.x1 / sg.u);
 
-  // queries as A fragments, in the order of dims that K's pieces give
-  uint32_t qa[D / 16][4];
-  float sc[2] = {a.scale, a.scale};
-  {
-    const __nv_bfloat16* qp[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int64_t f = static_cast<int64_t>(it.tile) * kTileRows + g + 8 * i;
-      const int hd = static_cast<int>(f % a.G);
-      qp[i] = rv[i].j >= 0 ? a.q + static_cast<int64_t>(q.row0 + rv[i].j) * a.q_ld + (h * a.G + hd) * D : nullptr;
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      constexpr int kPieces = D / 32;  // 16-byte pieces of a row a lane holds
-      uint4 w[kPieces];
-#pragma unroll
-      for (int c = 0; c < kPieces; ++c) {
-        const int piece = FP4 ? t * kPieces + c : 4 * c + t;
-        w[c] = qp[i] ? *reinterpret_cast<const uint4*>(qp[i] + piece * 8) : make_uint4(0u, 0u, 0u, 0u);
-      }
-      if (FP4) {
-        // over a power of two a row, into fp16
-        float v[D / 4];
-        float top = 0.f;
-#pragma unroll
-        for (int c = 0; c < kPieces; ++c) {
-          const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[c * 8 + 2 * e] = __uint_as_float(u[e] << 16);
-            v[c * 8 + 2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < D / 4; ++e) top = fmaxf(top, fabsf(v[e]));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int ex = (top > 0.f && top < INFINITY) ? max(-100, min(126, ilogbf(top))) : 0;
-        const float down = ldexpf(1.f, -ex);
-        sc[i] *= ldexpf(1.f, ex);
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          qa[s][i] = pack2(v[4 * s] * down, v[4 * s + 1] * down, true);
-          qa[s][2 + i] = pack2(v[4 * s + 2] * down, v[4 * s + 3] * down, true);
-        }
-      } else {
-#pragma unroll
-        for (int c = 0; c < kPieces; ++c) {
-          qa[2 * c][i] = w[c].x;
-          qa[2 * c][2 + i] = w[c].y;
-          qa[2 * c + 1][i] = w[c].z;
-          qa[2 * c + 1][2 + i] = w[c].w;
-        }
-      }
-    }
-  }
-
-  float o[kNT][4];
-#pragma unroll
-  for (int e = 0; e < kNT; ++e) o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
-  uint8_t* ring = smem + warp * kST * G_::kStage;
-  const uint32_t ring_u = smem_u32(ring);
-  const int* table = a.c.table + static_cast<int64_t>(it.s) * a.c.cols;
+  const int* table = a.c.table + static_cast<int64_t>(sg.s) * a.c.cols;
   auto unit_at = [&](int i) { return i < ur.nsink ? i : ur.first + (i - ur.nsink); };
   int pg[kSub];
   auto fetch_pages = [&](int i) {
@@ -256,6 +203,8 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
       else flag_status(a.r.status, DFLASH_STATUS_BAD_PAGE);
     }
   };
+  uint8_t* ring = smem + warp * kST * G_::kStage;
+  const uint32_t ring_u = smem_u32(ring);
   uint32_t pres = 0;  // of the units in flight, newest in the low bits: which 16-slot pieces are there
   auto issue = [&](int i, int stage) {
     pres <<= kSub;
@@ -299,10 +248,75 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
     issue(i0 + warp + s * kWarps, s);
     fetch_pages(i0 + warp + (s + 1) * kWarps);
   }
+
+  // queries as B fragments (row g of a block of 8), in the order of dims that K's pieces give
+  uint32_t qb[NB][D / 16][2];
+  float sc[NB][2];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const int64_t f = static_cast<int64_t>(sg.tile) * kTile + 8 * b + g;
+    const int j = static_cast<int>(f / a.G), hd = static_cast<int>(f - static_cast<int64_t>(j) * a.G);
+    const __nv_bfloat16* qp =
+        j < q.n ? a.q + static_cast<int64_t>(q.row0 + j) * a.q_ld + (h * a.G + hd) * D : nullptr;
+    constexpr int kPieces = D / 32;  // 16-byte pieces of a row a lane holds
+    uint4 w[kPieces];
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c) {
+      const int piece = FP4 ? t * kPieces + c : 4 * c + t;
+      w[c] = qp ? *reinterpret_cast<const uint4*>(qp + piece * 8) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (FP4) {
+      // over a power of two a row, into fp16
+      float top = 0.f;
+      float v[D / 4];
+#pragma unroll
+      for (int c = 0; c < kPieces; ++c) {
+        const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[c * 8 + 2 * e] = __uint_as_float(u[e] << 16);
+          v[c * 8 + 2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < D / 4; ++e) top = fmaxf(top, fabsf(v[e]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int ex = (top > 0.f && top < INFINITY) ? max(-100, min(126, ilogbf(top))) : 0;
+      const float down = ldexpf(1.f, -ex), up = a.scale * ldexpf(1.f, ex);
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+        qb[b][s][0] = pack2(v[4 * s] * down, v[4 * s + 1] * down, true);
+        qb[b][s][1] = pack2(v[4 * s + 2] * down, v[4 * s + 3] * down, true);
+      }
+      sc[b][0] = __shfl_sync(0xffffffffu, up, 8 * t);
+      sc[b][1] = __shfl_sync(0xffffffffu, up, 8 * t + 4);
+    } else {
+#pragma unroll
+      for (int c = 0; c < kPieces; ++c) {
+        qb[b][2 * c][0] = w[c].x;
+        qb[b][2 * c][1] = w[c].y;
+        qb[b][2 * c + 1][0] = w[c].z;
+        qb[b][2 * c + 1][1] = w[c].w;
+      }
+      sc[b][0] = sc[b][1] = a.scale;
+    }
+  }
+
+  float o[NB][kMT][4];
+  float m[NB][2], l[NB][2];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+#pragma unroll
+    for (int e = 0; e < kMT; ++e) o[b][e][0] = o[b][e][1] = o[b][e][2] = o[b][e][3] = 0.f;
+    m[b][0] = m[b][1] = -INFINITY;
+    l[b][0] = l[b][1] = 0.f;
+  }
+
   int stage = 0;
   for (int i = i0 + warp; i < i1; i += kWarps) {
     {
-      const int ns = stage + kST - 1 >= kST ? stage - 1 : stage + kST - 1;
+      const int ns = stage == 0 ? kST - 1 : stage - 1;
       issue(i + (kST - 1) * kWarps, ns);
       fetch_pages(i + kST * kWarps);
     }
@@ -313,119 +327,145 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
     const uint32_t here = (pres >> ((kST - 1) * kSub)) & ((1u << kSub) - 1u);
     const bool whole = here == (1u << kSub) - 1u && kb + kKeys <= q.C && (kb >= lo_max || kb + kKeys <= sinks);
 
-    // ------------------------------------------------ scores
-    float s[kKeys / 8][4];
+    // ------------------------------------------------ scores: keys on M, rows on N
+    float s[NB][kSub][4];
 #pragma unroll
-    for (int nt = 0; nt < kKeys / 8; ++nt) {
-      s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-      const int key = nt * 8 + g;
+    for (int kt = 0; kt < kSub; ++kt) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) s[b][kt][0] = s[b][kt][1] = s[b][kt][2] = s[b][kt][3] = 0.f;
+      const int k0 = kt * 16 + g, k1 = k0 + 8;
       if (!FP4) {
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
-          const uint4 w = *reinterpret_cast<const uint4*>(sp + key * kRow + swz<kRow>(key, 4 * c + t) * 16);
-          mma16816<FP4>(s[nt], qa[2 * c], w.x, w.y);
-          mma16816<FP4>(s[nt], qa[2 * c + 1], w.z, w.w);
+          const uint4 x = *reinterpret_cast<const uint4*>(sp + k0 * kRow + swz<kRow>(k0, 4 * c + t) * 16);
+          const uint4 y = *reinterpret_cast<const uint4*>(sp + k1 * kRow + swz<kRow>(k1, 4 * c + t) * 16);
+          const uint32_t f0[4] = {x.x, y.x, x.y, y.y}, f1[4] = {x.z, y.z, x.w, y.w};
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            mma16816<FP4>(s[b][kt], f0, qb[b][2 * c][0], qb[b][2 * c][1]);
+            mma16816<FP4>(s[b][kt], f1, qb[b][2 * c + 1][0], qb[b][2 * c + 1][1]);
+          }
         }
       } else {
         constexpr int kW = D / 32;  // words a lane holds of a key
-        uint32_t w[kW];
-        const uint8_t* src = sp + key * kRow + (D == 128 ? swz<kRow>(key, t) * 16 : t * (D / 8));
-        if (D == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(src);
-          w[0] = x.x;
-          w[1 % kW] = x.y;
-          w[2 % kW] = x.z;
-          w[3 % kW] = x.w;
-        } else if (D == 64) {
-          const uint2 x = *reinterpret_cast<const uint2*>(src);
-          w[0] = x.x;
-          w[1 % kW] = x.y;
-        } else {
-          w[0] = *reinterpret_cast<const uint32_t*>(src);
+        uint32_t w[2][kW], gs[2][2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int key = x ? k1 : k0;
+          const uint8_t* src = sp + key * kRow + (D == 128 ? swz<kRow>(key, t) * 16 : t * (D / 8));
+          if (D == 128) {
+            const uint4 u = *reinterpret_cast<const uint4*>(src);
+            w[x][0] = u.x;
+            w[x][1 % kW] = u.y;
+            w[x][2 % kW] = u.z;
+            w[x][3 % kW] = u.w;
+          } else if (D == 64) {
+            const uint2 u = *reinterpret_cast<const uint2*>(src);
+            w[x][0] = u.x;
+            w[x][1 % kW] = u.y;
+          } else {
+            w[x][0] = *reinterpret_cast<const uint32_t*>(src);
+          }
+          const uint8_t* scp = sp + G_::kOffKs + key * G_::kSc;
+          uint32_t two;  // the lane's one or two group scales
+          if (D == 128) two = *reinterpret_cast<const uint16_t*>(scp + 2 * t);
+          else two = scp[D == 64 ? t : t >> 1] * 0x101u;
+          const uint32_t s2 = e4m3x2(two);
+          gs[x][0] = __byte_perm(s2, 0, 0x1010);
+          gs[x][1] = __byte_perm(s2, 0, 0x3232);
         }
-        const uint8_t* scp = sp + G_::kOffKs + key * G_::kSc;
-        uint32_t two;  // the lane's one or two group scales
-        if (D == 128) two = *reinterpret_cast<const uint16_t*>(scp + 2 * t);
-        else two = scp[D == 64 ? t : t >> 1] * 0x101u;
-        const uint32_t sp2 = e4m3x2(two);
-        const uint32_t g0 = __byte_perm(sp2, 0, 0x1010), g1 = __byte_perm(sp2, 0, 0x3232);
 #pragma unroll
         for (int x = 0; x < kW; ++x) {
-          uint32_t f[4];
-          e2m1x8(w[x], f);
-          const uint32_t gs = (D == 128 && x >= 2) ? g1 : g0;
-          mma16816<FP4>(s[nt], qa[2 * x], hmul2(f[0], gs), hmul2(f[1], gs));
-          mma16816<FP4>(s[nt], qa[2 * x + 1], hmul2(f[2], gs), hmul2(f[3], gs));
+          uint32_t f[2][4];
+          e2m1x8(w[0][x], f[0]);
+          e2m1x8(w[1][x], f[1]);
+          const int gi = (D == 128 && x >= 2) ? 1 : 0;
+          const uint32_t f0[4] = {hmul2(f[0][0], gs[0][gi]), hmul2(f[1][0], gs[1][gi]), hmul2(f[0][1], gs[0][gi]),
+                                  hmul2(f[1][1], gs[1][gi])};
+          const uint32_t f1[4] = {hmul2(f[0][2], gs[0][gi]), hmul2(f[1][2], gs[1][gi]), hmul2(f[0][3], gs[0][gi]),
+                                  hmul2(f[1][3], gs[1][gi])};
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            mma16816<FP4>(s[b][kt], f0, qb[b][2 * x][0], qb[b][2 * x][1]);
+            mma16816<FP4>(s[b][kt], f1, qb[b][2 * x + 1][0], qb[b][2 * x + 1][1]);
+          }
         }
       }
     }
     if (!whole) {
 #pragma unroll
-      for (int nt = 0; nt < kKeys / 8; ++nt)
+      for (int kt = 0; kt < kSub; ++kt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const bool there = (here >> (nt >> 1)) & 1u;
-          if (!there || !sees(a, q, rv[e >> 1], kb + nt * 8 + 2 * t + (e & 1))) s[nt][e] = -INFINITY;
+          const bool there = (here >> kt) & 1u;
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            if (!there || !sees(a, q, rv[b][e & 1], kb + kt * 16 + g + 8 * (e >> 1))) s[b][kt][e] = -INFINITY;
         }
     }
 
-    // ------------------------------------------------ running maximum and sum
-    float mx[2] = {-INFINITY, -INFINITY};
+    // ------------------------------------------------ running maximum and sum, weights
+    uint32_t pb[NB][kSub][2];
 #pragma unroll
-    for (int nt = 0; nt < kKeys / 8; ++nt) {
-      mx[0] = fmaxf(mx[0], fmaxf(s[nt][0], s[nt][1]));
-      mx[1] = fmaxf(mx[1], fmaxf(s[nt][2], s[nt][3]));
-    }
-    bool moved = false;
-    float al[2], sub[2];
+    for (int b = 0; b < NB; ++b) {
+      float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-    for (int i2 = 0; i2 < 2; ++i2) {
-      mx[i2] = fmaxf(mx[i2], __shfl_xor_sync(0xffffffffu, mx[i2], 1));
-      mx[i2] = fmaxf(mx[i2], __shfl_xor_sync(0xffffffffu, mx[i2], 2));
-      const float mn = fmaxf(m[i2], mx[i2] * sc[i2]);
-      al[i2] = m[i2] == mn ? 1.f : ex2f(m[i2] - mn);
-      moved |= m[i2] != mn;
-      m[i2] = mn;
-      sub[i2] = mn == -INFINITY ? 0.f : mn - G_::kShift;
-    }
-    if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-      for (int e = 0; e < kNT; ++e) {
-        o[e][0] *= al[0];
-        o[e][1] *= al[0];
-        o[e][2] *= al[1];
-        o[e][3] *= al[1];
+      for (int kt = 0; kt < kSub; ++kt) {
+        mx[0] = fmaxf(mx[0], fmaxf(s[b][kt][0], s[b][kt][2]));
+        mx[1] = fmaxf(mx[1], fmaxf(s[b][kt][1], s[b][kt][3]));
       }
-      l[0] *= al[0];
-      l[1] *= al[1];
-    }
-    uint32_t pa[kSub][4];
+      bool moved = false;
+      float al[2], sub[2];
 #pragma unroll
-    for (int nt = 0; nt < kKeys / 8; ++nt) {
+      for (int x = 0; x < 2; ++x) {
+        mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 4));
+        mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 8));
+        mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 16));
+        const float mn = fmaxf(m[b][x], mx[x] * sc[b][x]);
+        al[x] = m[b][x] == mn ? 1.f : ex2f(m[b][x] - mn);
+        moved |= m[b][x] != mn;
+        m[b][x] = mn;
+        sub[x] = mn == -INFINITY ? 0.f : mn - G_::kShift;
+      }
+      if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[nt][e] = ex2f(fmaf(s[nt][e], sc[e >> 1], -sub[e >> 1]));
-      l[0] += s[nt][0] + s[nt][1];
-      l[1] += s[nt][2] + s[nt][3];
-      // P to 16 bits for the matrix product (the sum keeps fp32 P): bf16, or
-      // fp16 beside 4-bit values
-      pa[nt >> 1][(nt & 1) * 2] = pack2(s[nt][0], s[nt][1], FP4);
-      pa[nt >> 1][(nt & 1) * 2 + 1] = pack2(s[nt][2], s[nt][3], FP4);
+        for (int e = 0; e < kMT; ++e) {
+          o[b][e][0] *= al[0];
+          o[b][e][1] *= al[1];
+          o[b][e][2] *= al[0];
+          o[b][e][3] *= al[1];
+        }
+        l[b][0] *= al[0];
+        l[b][1] *= al[1];
+      }
+#pragma unroll
+      for (int kt = 0; kt < kSub; ++kt) {
+        float* x = s[b][kt];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = ex2f(fmaf(x[e], sc[b][e & 1], -sub[e & 1]));
+        l[b][0] += x[0] + x[2];
+        l[b][1] += x[1] + x[3];
+        // P to 16 bits for the matrix product (the sum keeps fp32 P): bf16, or
+        // fp16 beside 4-bit values; from (key, rows) to (row, keys)
+        pb[b][kt][0] = transpose8(pack2(x[0], x[1], FP4));
+        pb[b][kt][1] = transpose8(pack2(x[2], x[3], FP4));
+      }
     }
 
-    // ------------------------------------------------ output
+    // ------------------------------------------------ output: dims on M, rows on N
 #pragma unroll
-    for (int b = 0; b < kSub; ++b) {
+    for (int kt = 0; kt < kSub; ++kt) {
       // slots that no row of the tile sees may hold anything: their V counts as zero
       uint32_t live[2] = {0xffffffffu, 0xffffffffu};  // of the key pairs (2t, 2t+1) and (2t+8, 2t+9), 16 bits a key
       if (!whole) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const int slot = kb + 16 * b + 2 * t + (x & 1) + (x >> 1) * 8;
-          const bool ok = ((here >> b) & 1u) && ((slot >= lo && slot < hi) || slot < sinks);
+          const int slot = kb + 16 * kt + 2 * t + (x & 1) + (x >> 1) * 8;
+          const bool ok = ((here >> kt) & 1u) && ((slot >= lo && slot < hi) || slot < sinks);
           if (!ok) live[x >> 1] &= (x & 1) ? 0x0000ffffu : 0xffff0000u;
         }
       }
-      const uint8_t* vp = sp + G_::kOffV + b * 16 * kRow;
+      const uint8_t* vp = sp + G_::kOffV + kt * 16 * kRow;
       if (!FP4) {
         constexpr int kC = D >= 64 ? D / 64 : 1;
         constexpr int kWords = D >= 64 ? 4 : 2;
@@ -449,16 +489,18 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
             }
           }
 #pragma unroll
-          for (int e = 0; e < 2 * kWords; ++e) {
-            const unsigned sel = (e & 1) ? 0x7632u : 0x5410u;
-            const uint32_t b0 = __byte_perm(w[0][e >> 1], w[1][e >> 1], sel) & live[0];
-            const uint32_t b1 = __byte_perm(w[2][e >> 1], w[3][e >> 1], sel) & live[1];
-            mma16816<FP4>(o[c * 8 + e], pa[b], b0, b1);
+          for (int e = 0; e < kWords; ++e) {
+            const uint32_t f[4] = {
+                __byte_perm(w[0][e], w[1][e], 0x5410) & live[0], __byte_perm(w[0][e], w[1][e], 0x7632) & live[0],
+                __byte_perm(w[2][e], w[3][e], 0x5410) & live[1], __byte_perm(w[2][e], w[3][e], 0x7632) & live[1]};
+#pragma unroll
+            for (int b = 0; b < NB; ++b) mma16816<FP4>(o[b][c * 4 + e], f, pb[b][kt][0], pb[b][kt][1]);
           }
         }
       } else {
         constexpr int kB = D / 16;  // bytes a lane holds of a key: dims (D/8) g ..
-        uint32_t w[4][(kB + 3) / 4];
+        constexpr int kVW = (kB + 3) / 4;
+        uint32_t w[4][kVW];
         uint32_t vsc[2];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
@@ -467,7 +509,7 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
             const uint2 u =
                 *reinterpret_cast<const uint2*>(vp + key * kRow + swz<kRow>(key, g >> 1) * 16 + (g & 1) * 8);
             w[x][0] = u.x;
-            w[x][1 % ((kB + 3) / 4)] = u.y;
+            w[x][1 % kVW] = u.y;
           } else if (D == 64) {
             w[x][0] = *reinterpret_cast<const uint32_t*>(vp + key * kRow + g * 4);
           } else {
@@ -476,21 +518,23 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const uint8_t* vscp = sp + G_::kOffVs + (b * 16 + 2 * t + 8 * x) * G_::kSc + (g * (D / 8)) / 16;
+          const uint8_t* vscp = sp + G_::kOffVs + (kt * 16 + 2 * t + 8 * x) * G_::kSc + (g * (D / 8)) / 16;
           vsc[x] = e4m3x2(vscp[0] | (static_cast<uint32_t>(vscp[G_::kSc]) << 8)) & live[x];
         }
 #pragma unroll
-        for (int x = 0; x < (kB + 3) / 4; ++x) {
+        for (int x = 0; x < kVW; ++x) {
           uint32_t f[4][4];
 #pragma unroll
           for (int k2 = 0; k2 < 4; ++k2) e2m1x8(w[k2][x], f[k2]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (x * 8 + e >= kNT) continue;
-            const unsigned sel = (e & 1) ? 0x7632u : 0x5410u;
-            const uint32_t b0 = hmul2(__byte_perm(f[0][e >> 1], f[1][e >> 1], sel), vsc[0]);
-            const uint32_t b1 = hmul2(__byte_perm(f[2][e >> 1], f[3][e >> 1], sel), vsc[1]);
-            mma16816<FP4>(o[x * 8 + e], pa[b], b0, b1);
+          for (int e = 0; e < 4; ++e) {
+            if (x * 4 + e >= kMT) continue;
+            const uint32_t v[4] = {hmul2(__byte_perm(f[0][e], f[1][e], 0x5410), vsc[0]),
+                                   hmul2(__byte_perm(f[0][e], f[1][e], 0x7632), vsc[0]),
+                                   hmul2(__byte_perm(f[2][e], f[3][e], 0x5410), vsc[1]),
+                                   hmul2(__byte_perm(f[2][e], f[3][e], 0x7632), vsc[1])};
+#pragma unroll
+            for (int b = 0; b < NB; ++b) mma16816<FP4>(o[b][x * 4 + e], v, pb[b][kt][0], pb[b][kt][1]);
           }
         }
       }
@@ -500,64 +544,65 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
   }
   cp_wait<0>();
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-  }
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[b][i] += __shfl_xor_sync(0xffffffffu, l[b][i], 4);
+      l[b][i] += __shfl_xor_sync(0xffffffffu, l[b][i], 8);
+      l[b][i] += __shfl_xor_sync(0xffffffffu, l[b][i], 16);
+    }
   __syncthreads();
 
   // ---------------------------------------------------- join the warps' parts
   float* po = reinterpret_cast<float*>(smem);
-  float* pml = po + kWarps * kTileRows * G_::kPartLd;
-  // n-tile e of output half c, column 2t + x of the tile: the dim it holds
-  constexpr int kPer = (!FP4 && D == 128) ? 8 : kNT;  // n-tiles of consecutive dims
+  float* pml = po + kWarps * kTile * G_::kPartLd;
+  // m-tile e of row block b: dims base(e) + {0, 1} of rows 2t, 2t + 1
+  constexpr int kPer = (!FP4 && D == 128) ? 4 : kMT;  // m-tiles of a lane's consecutive dims
 #pragma unroll
-  for (int e = 0; e < kNT; ++e) {
-    const int c = e / kPer, r = e % kPer;
-    const int d0 = c * 64 + kPer * 2 * t + r;
+  for (int b = 0; b < NB; ++b)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float* row = po + (warp * kTileRows + g + 8 * i) * G_::kPartLd;
-      row[d0] = o[e][2 * i];
-      row[d0 + kPer] = o[e][2 * i + 1];
+    for (int e = 0; e < kMT; ++e) {
+      const int d0 = (e / kPer) * 64 + 2 * kPer * g + 2 * (e % kPer);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        *reinterpret_cast<float2*>(po + (warp * kTile + 8 * b + 2 * t + i) * G_::kPartLd + d0) =
+            make_float2(o[b][e][i], o[b][e][2 + i]);
     }
-  }
-  if (t == 0) {
+  if (g == 0) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      pml[(warp * kTileRows + g + 8 * i) * 2] = m[i];
-      pml[(warp * kTileRows + g + 8 * i) * 2 + 1] = l[i];
-    }
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        pml[(warp * kTile + 8 * b + 2 * t + i) * 2] = m[b][i];
+        pml[(warp * kTile + 8 * b + 2 * t + i) * 2 + 1] = l[b][i];
+      }
   }
   __syncthreads();
-  const bool keep = it.ns > 1 && it.slot < a.slots;
-  for (int x = threadIdx.x; x < kTileRows * (D / 4); x += kWarps * 32) {
+  for (int x = threadIdx.x; x < kTile * (D / 4); x += kWarps * 32) {
     const int r = x / (D / 4), d4 = (x % (D / 4)) * 4;
-    const int64_t f = static_cast<int64_t>(it.tile) * kTileRows + r;
+    const int64_t f = static_cast<int64_t>(sg.tile) * kTile + r;
     const int j = static_cast<int>(f / a.G);
     if (j >= q.n) continue;
     float M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, pml[(w * kTileRows + r) * 2]);
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, pml[(w * kTile + r) * 2]);
     float den = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (M != -INFINITY) {
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float wt = ex2f(pml[(w * kTileRows + r) * 2] - M);
-        const float4 v = *reinterpret_cast<const float4*>(po + (w * kTileRows + r) * G_::kPartLd + d4);
-        den = fmaf(wt, pml[(w * kTileRows + r) * 2 + 1], den);
+        const float wt = ex2f(pml[(w * kTile + r) * 2] - M);
+        const float4 v = *reinterpret_cast<const float4*>(po + (w * kTile + r) * G_::kPartLd + d4);
+        den = fmaf(wt, pml[(w * kTile + r) * 2 + 1], den);
         acc.x = fmaf(wt, v.x, acc.x);
         acc.y = fmaf(wt, v.y, acc.y);
         acc.z = fmaf(wt, v.z, acc.z);
         acc.w = fmaf(wt, v.w, acc.w);
       }
     }
-    if (it.ns > 1) {
-      if (!keep) continue;
-      const int64_t row = (static_cast<int64_t>(it.slot) * a.c.nkv + h) * kTileRows + r;
-      *reinterpret_cast<float4*>(a.part_o + row * D + d4) = acc;
-      if (d4 == 0) *reinterpret_cast<float2*>(a.part_ml + row * 2) = make_float2(M, den);
+    if (part) {
+      *reinterpret_cast<float4*>(a.part_o + (part_row + r) * D + d4) = acc;
+      if (d4 == 0) *reinterpret_cast<float2*>(a.part_ml + (part_row + r) * 2) = make_float2(M, den);
     } else {
       const int hd = static_cast<int>(f - static_cast<int64_t>(j) * a.G);
       const float inv = M == -INFINITY ? 0.f : 1.f / den;
@@ -567,48 +612,65 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
       *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(q.row0 + j) * a.out_ld + (h * a.G + hd) * D + d4) = w;
     }
   }
+  __syncthreads();  // the next segment uses the ring and `run` again
+  }
 }
 
-// Joins the slices of a row: one warp a row of a split tile.
-constexpr int kCombineRows = 4;
+// Joins the parts of the tiles that a boundary between two CTAs' shares cuts:
+// a CTA a boundary and rows of its tile, a warp a row.
+constexpr int kCombineRows = 8;
 template <int D>
 __global__ void __launch_bounds__(kCombineRows * 32) page_combine_kernel(const __grid_constant__ PageAttnArgs a) {
   constexpr int kE = D / 32;
-  __shared__ Item item_s;
-  __shared__ int have_s;
+  __shared__ Segment seg_s;
+  __shared__ int slot_s, parts_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // row_start and lens were complete before the attention kernel let this one start
   if (warp == 0) {
-    Item it;
-    const bool have = find_item(a, static_cast<int>(blockIdx.x), true, &it);
+    int parts = 0, slot = 0;
+    const Share sh = share_of(a);
+    const long long b = blockIdx.x + 1ll;
+    Segment sg{};
+    if (!sh.whole && b < sh.ctas) {
+      const long long at = sh.start(a, b);
+      sg = segment_at(a, sh, at);
+      const long long from = at - sg.x0, to = from + sg.u, before = sh.start(a, b - 1);
+      if (sg.x0 > 0 && before <= from) {  // the first boundary inside the tile
+        slot = static_cast<int>(2 * (b - 1) + (before == from ? 0 : 1));
+        parts = 2;
+        while (b + parts - 1 < sh.ctas && sh.start(a, b + parts - 1) < to) ++parts;
+      }
+    }
     if (lane == 0) {
-      item_s = it;
-      have_s = have;
+      seg_s = sg;
+      slot_s = slot;
+      parts_s = parts;
     }
   }
   pdl_wait();
   pdl_trigger();
   __syncthreads();
-  if (!have_s) return;
-  const Item it = item_s;
-  const int h = blockIdx.y, r = blockIdx.z * kCombineRows + warp;
+  const int parts = parts_s;
+  if (parts == 0) return;
+  const Segment sg = seg_s;
+  const int r = blockIdx.y * kCombineRows + warp;
   bool bad;
-  const StreamRows q = stream_rows(a.r, it.s, &bad);
-  const int64_t f = static_cast<int64_t>(it.tile) * a.tile + r;
+  const StreamRows q = stream_rows(a.r, sg.s, &bad);
+  const int64_t f = static_cast<int64_t>(sg.tile) * a.tile + r;
   const int j = static_cast<int>(f / a.G);
-  if (r >= a.tile || j >= q.n || it.slot + it.ns > a.slots) return;
-  const int64_t row0 = (static_cast<int64_t>(it.slot) * a.c.nkv + h) * a.tile + r;
-  const int64_t step = static_cast<int64_t>(a.c.nkv) * a.tile;
+  if (r >= a.tile || j >= q.n) return;
+  const int next = 2 * (static_cast<int>(blockIdx.x) + 1);  // slot of the second part; the others follow by 2
+  auto row_of = [&](int k) { return static_cast<int64_t>(k == 0 ? slot_s : next + 2 * (k - 1)) * a.tile + r; };
   float M = -INFINITY;
-  for (int k = lane; k < it.ns; k += 32) M = fmaxf(M, a.part_ml[(row0 + k * step) * 2]);
+  for (int k = lane; k < parts; k += 32) M = fmaxf(M, a.part_ml[row_of(k) * 2]);
 #pragma unroll
   for (int x = 16; x >= 1; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
   float acc[kE] = {};
   float den = 0.f;
   if (M != -INFINITY) {
 #pragma unroll 8
-    for (int k = 0; k < it.ns; ++k) {
-      const int64_t row = row0 + k * step;
+    for (int k = 0; k < parts; ++k) {
+      const int64_t row = row_of(k);
       const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + row * 2);
       const float w = ex2f(ml.x - M);
       den = fmaf(w, ml.y, den);
@@ -623,7 +685,7 @@ __global__ void __launch_bounds__(kCombineRows * 32) page_combine_kernel(const _
   }
   const float inv = M == -INFINITY ? 0.f : 1.f / den;
   const int hd = static_cast<int>(f - static_cast<int64_t>(j) * a.G);
-  __nv_bfloat16* dst = a.out + static_cast<int64_t>(q.row0 + j) * a.out_ld + (h * a.G + hd) * D + lane * kE;
+  __nv_bfloat16* dst = a.out + static_cast<int64_t>(q.row0 + j) * a.out_ld + (sg.h * a.G + hd) * D + lane * kE;
   if (kE == 4) {
     uint2 w;
     w.x = pack2(acc[0] * inv, acc[1 % kE] * inv, false);
@@ -636,24 +698,33 @@ __global__ void __launch_bounds__(kCombineRows * 32) page_combine_kernel(const _
   }
 }
 
-template <int D, bool FP4>
+// A kernel's shared-memory limit, raised once a device.
+int raise_smem(const void* kern, int bytes) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess ? DFLASH_OK
+                                                                                                       : DFLASH_E_CUDA;
+}
+
+template <int D, bool FP4, int NB>
 int launch_small(const PageAttnArgs& a, const PagePlan& p, cudaStream_t st) {
-  using G_ = Geo<D, FP4>;
-  auto kern = page_attn_kernel<D, FP4>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G_::kSmem) != cudaSuccess) {
-    cudaGetLastError();
-    return DFLASH_E_CUDA;
-  }
-  const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(p.items), static_cast<unsigned>(a.c.nkv)),
-                                   dim3(kWarps * 32), G_::kSmem, st, a);
+  using G_ = Geo<D, FP4, NB>;
+  auto kern = page_attn_kernel<D, FP4, NB>;
+  const int rc = raise_smem(reinterpret_cast<const void*>(kern), G_::kSmem);
+  if (rc) return rc;
+  const cudaError_t e =
+      launch_pdl(kern, dim3(static_cast<unsigned>(p.ctas)), dim3(kWarps * 32), G_::kSmem, st, a);
   count_launch();
   return cuda_status(e);
+}
+template <int D>
+int launch_small_any(const PageAttnArgs& a, const PagePlan& p, bool fp4, cudaStream_t st) {
+  if (p.tile == 8) return fp4 ? launch_small<D, true, 1>(a, p, st) : launch_small<D, false, 1>(a, p, st);
+  return fp4 ? launch_small<D, true, 2>(a, p, st) : launch_small<D, false, 2>(a, p, st);
 }
 
 template <int D>
 int launch_combine(const PageAttnArgs& a, const PagePlan& p, cudaStream_t st) {
   const cudaError_t e = launch_pdl(page_combine_kernel<D>,
-                                   dim3(static_cast<unsigned>(p.split_tiles), static_cast<unsigned>(a.c.nkv),
+                                   dim3(static_cast<unsigned>(p.target - 1),
                                         static_cast<unsigned>((a.tile + kCombineRows - 1) / kCombineRows)),
                                    dim3(kCombineRows * 32), 0, st, a);
   count_launch();
@@ -667,29 +738,26 @@ PagePlan page_attention_plan(const dflash_pages& c, const dflash_rows& r, int nq
   const bool fp4 = c.format == DFLASH_PAGES_FP4;
   PagePlan p{};
   const int64_t R = static_cast<int64_t>(r.max_rows) * G;
-  p.tc = c.head_dim >= 64 && R > kTileRows;
+  p.tc = c.head_dim >= 64 && R > 16;
   if (p.tc) {
     p.tile = R > 512 ? 256 : 128;
     p.unit = 128;
     p.target = 152;
     p.min_units = 4;
+    p.no_split = 4;
   } else {
-    p.tile = kTileRows;
+    p.tile = R > 8 ? 16 : 8;
     p.unit = fp4 ? 32 : 16;
     p.target = 152 * (fp4 ? 2 : 1);
     p.min_units = 2 * kWarps;
+    p.no_split = 4 * kWarps;
   }
-  const int64_t per_stream = (static_cast<int64_t>(r.max_rows) * G + p.tile - 1) / p.tile;
+  const int64_t per_stream = (R + p.tile - 1) / p.tile;
   const int64_t by_rows = (static_cast<int64_t>(r.rows) * G + p.tile - 1) / p.tile + c.streams;
-  const int64_t tiles = std::min(c.streams * per_stream, by_rows);
-  // a stream is split only when its units pass total / target, so all its
-  // slices are under twice the target; slices of at most the whole table
-  const int64_t cap_units = (static_cast<int64_t>(c.table_cols) * c.page_size + p.unit - 1) / p.unit + 1;
-  const bool may_split = cap_units > p.min_units;
-  const int64_t per_head = (p.target + c.n_kv_heads - 1) / c.n_kv_heads;
-  p.items = tiles + (may_split ? per_head : 0);
-  p.slots = may_split ? static_cast<int>(2 * per_head + 1) : 0;
-  p.split_tiles = may_split ? std::min(tiles, per_head) : 0;
+  const int64_t tiles = std::min(c.streams * per_stream, by_rows) * c.n_kv_heads;
+  const int64_t units = (static_cast<int64_t>(c.table_cols) * c.page_size + p.unit - 1) / p.unit;
+  p.split = units > p.no_split;
+  p.ctas = std::max<int64_t>(tiles, p.split ? p.target : 0);
   return p;
 }
 
@@ -698,12 +766,12 @@ int launch_page_attention(const PageAttnArgs& a, const PagePlan& p, bool fp4, cu
   int rc;
   {
     TraceScope ts(st, "page_attention", 0.0, 0.0);
-    if (p.tc) rc = launch_page_attention_tc(a, p, fp4, st);
-    else if (D == 128) rc = fp4 ? launch_small<128, true>(a, p, st) : launch_small<128, false>(a, p, st);
-    else if (D == 64) rc = fp4 ? launch_small<64, true>(a, p, st) : launch_small<64, false>(a, p, st);
-    else rc = fp4 ? launch_small<32, true>(a, p, st) : launch_small<32, false>(a, p, st);
+    rc = p.tc ? launch_page_attention_tc(a, p, fp4, st)
+         : D == 128 ? launch_small_any<128>(a, p, fp4, st)
+         : D == 64 ? launch_small_any<64>(a, p, fp4, st)
+                   : launch_small_any<32>(a, p, fp4, st);
   }
-  if (rc || p.split_tiles == 0) return rc;
+  if (rc || !p.split) return rc;
   TraceScope ts(st, "page_combine", 0.0, 0.0);
   return D == 128 ? launch_combine<128>(a, p, st) : D == 64 ? launch_combine<64>(a, p, st) : launch_combine<32>(a, p, st);
 }

@@ -49,7 +49,7 @@ struct TcGeo {
   static constexpr int kSlot = kTK * D * 2;                 // a K or V tile
   static constexpr int kQ = (PAIR ? 2 : 1) * kMRows * D * 2;
   static constexpr int kRow = D / 2, kSc = D / 16;          // 4-bit row and scale bytes
-  static constexpr int kRaw = FP4 ? kTK * (kRow + 8) : 0;   // a staged 4-bit tile (scales padded to 8 bytes)
+  static constexpr int kRaw = FP4 ? kTK * (kRow + (kSc > 8 ? kSc : 8)) : 0;  // a staged 4-bit tile
   static constexpr int kStage = FP4 ? (PAIR ? 3 : 6) : 0;   // staged tiles
   static constexpr int kSlots = D == 64 ? 8 : FP4 ? 4 : (PAIR ? 5 : 6);
   static constexpr int kOffSlots = kQ;
@@ -187,22 +187,25 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
   uint64_t* o_full = q_full + 1;     // every MMA is done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 1);
   int* abort_word = reinterpret_cast<int*>(tmem_slot + 1);
-  int* have_s = abort_word + 1;
-  Item* item_s = reinterpret_cast<Item*>(have_s + 1);
+  Run* run = reinterpret_cast<Run*>(smem + Ge::kOffBar + 256);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.y;
   int* err = a.r.status;
 
   pdl_wait();
   pdl_trigger();
-  if (warp == 0) {
-    Item it;
-    const bool have = find_item(a, static_cast<int>(blockIdx.x), false, &it);
-    if (lane == 0) {
-      *item_s = it;
-      *have_s = have;
-    }
+  if (warp == 0) run_begin(a, run);
+  __syncthreads();
+  const bool any_work = run->at < run->end;
+  __syncthreads();  // every warp has read it before the run moves on
+  if (!any_work) return;
+  if (warp == 8) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
   }
+  for (bool first = true;; first = false) {
+  // between segments everything asynchronous has completed: the barriers start
+  // again at phase 0
+  if (warp == 0) run_next(a, run);
   if (threadIdx.x == 32) {
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&full[s], FP4 ? 32 * Ge::kProd : 1);
@@ -214,20 +217,18 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
     }
     mbar_init(q_full, PAIR ? 2 * kMRows : kMRows);
     mbar_init(o_full, 1);
-    *abort_word = 0;
+    if (first) *abort_word = 0;
     fence_barrier_init();
-  }
-  __syncthreads();
-  if (!*have_s) return;
-  const Item it = *item_s;
-  if (warp == 8) {
-    tmem_alloc(tmem_slot, 512);
-    tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (!run->left) break;
   const uint32_t tmem = *tmem_slot;
+  const Segment it = run->seg;
+  const int h = it.h;
+  const bool split = it.x0 > 0 || it.x1 < it.u;
+  const int64_t part_row = (2ll * blockIdx.x + (first ? 0 : 1)) * a.tile;
 
   bool bad;
   const StreamRows q = stream_rows(a.r, it.s, &bad);
@@ -256,8 +257,8 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
   // slots below this are seen by every row as far as the rows' order goes
   const int all_end = !plain ? q.C : a.mode == DFLASH_MASK_CAUSAL ? q.C + j_lo + 1 : q.C + q.n;
   const UnitRange ur = unit_range(lo, hi, a.sinks, kTK);
-  const int i0 = static_cast<int>(static_cast<long long>(ur.n) * it.split / it.ns);
-  const int i1 = static_cast<int>(static_cast<long long>(ur.n) * (it.split + 1) / it.ns);
+  const int i0 = static_cast<int>(static_cast<long long>(ur.n) * it.x0 / it.u);
+  const int i1 = static_cast<int>(static_cast<long long>(ur.n) * it.x1 / it.u);
   const int nt = i1 - i0;  // key tiles
   auto slot0 = [&](int t) {
     const int i = i0 + t;
@@ -333,7 +334,8 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
     // V rows no row sees: whatever the slots hold, they count as zero (4-bit
     // tiles are written clean)
     auto clean = [&](int sl, int kb) {
-      if (FP4 || inside(kb)) return;
+      if constexpr (FP4) return;
+      if (inside(kb)) return;
       for (int r = 0; r < kTK; ++r) {
         if (live(kb + r)) continue;
         uint8_t* row = smem + Ge::kOffSlots + sl * Ge::kSlot + r * 128;
@@ -726,10 +728,9 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
       const float w0 = mine && m != -INFINITY ? ex2f(m - M) : 0.f;
       const float w1 = m1 != -INFINITY ? ex2f(m1 - M) : 0.f;
       const float den = (w0 > 0.f ? w0 * l : 0.f) + (w1 > 0.f ? w1 * l1 : 0.f);
-      const bool split = it.ns > 1;
       const float inv = split ? 1.f : M == -INFINITY ? 0.f : 1.f / den;
-      const bool write = rv.j >= 0 && (!split || it.slot < a.slots);
-      const int64_t prow = (static_cast<int64_t>(it.slot) * a.c.nkv + h) * a.tile + (PAIR ? s * kMRows : 0) + r;
+      const bool write = rv.j >= 0;
+      const int64_t prow = part_row + (PAIR ? s * kMRows : 0) + r;
       __nv_bfloat16* dst = a.out + static_cast<int64_t>(q.row0 + jr) * a.out_ld + (h * a.G + hd) * D;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
@@ -768,9 +769,14 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
     }
     tc_fence_before();
   }
+  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  if (warp == 8) tmem_dealloc(tmem, 512);
+  if (threadIdx.x == 32) {
+    for (uint64_t* b = full; b <= o_full; ++b)
+      asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(b)) : "memory");
+  }
+  }
+  if (warp == 8) tmem_dealloc(*tmem_slot, 512);
 }
 
 template <int D, bool FP4, bool PAIR>
@@ -783,8 +789,7 @@ int launch(const TcPageArgs& P, const PagePlan& p, cudaStream_t st) {
     cudaGetLastError();
     return DFLASH_E_CUDA;
   }
-  const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(p.items), static_cast<unsigned>(P.a.c.nkv)),
-                                   dim3(Ge::kThreads), kBytes, st, P);
+  const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(p.ctas)), dim3(Ge::kThreads), kBytes, st, P);
   count_launch();
   return cuda_status(e);
 }

@@ -37,14 +37,14 @@ struct PageAttnArgs {
   int mask_ld, mode, window, sinks;
   int nq, G;
   float scale;           // softmax scale times log2(e)
-  // work split: an item is one (stream, tile of rows, slice of the keys)
+  // work split (see Share)
   int unit;              // slots a unit of the split
   int tile;              // rows (query row x head of the group) a tile
-  int target;            // items over all kv heads the split aims at
-  int min_units;         // fewest units an item is given
-  int slots;             // partial slots a kv head in part_o
-  float* part_o;         // [slots][nkv][tile][d]
-  float* part_ml;        // [slots][nkv][tile][2]
+  int target;            // CTAs of one wave
+  int min_units;         // fewest units a CTA's share has
+  int no_split;          // tiles of up to this many units are not split
+  float* part_o;         // [2 * target][tile][d]; null: nothing is split
+  float* part_ml;        // [2 * target][tile][2]
 };
 
 __device__ __forceinline__ void flag_status(int* status, int bits) {
@@ -80,81 +80,140 @@ __device__ __forceinline__ UnitRange unit_range(int lo, int hi, int sinks, int u
   return u;
 }
 
-// The split of a call's work, the same in every CTA of a call. A stream of n
-// rows is mt tiles of `tile` (row, head) pairs; each tile's units are cut into
-// ns slices, about total / target units each, so that streams of unequal
-// length give slices of equal length.
-struct Item {
-  int s, tile, split, ns, slot;  // slot: partial slot (ns > 1)
+// The split of a call's work, the same in every CTA of a call. Each stream of
+// n rows is mt tiles of `tile` (row, head) pairs; a tile's keys are the
+// stream's units. All tiles' units, kv head by kv head, stream by stream, make
+// one line, and CTA b of B takes the part [total * b / B, total * (b + 1) / B)
+// of it: streams of unequal length make equal shares. A share is a run of
+// segments, each (part of) one tile; a part goes to the workspace, slot 2b for
+// a CTA's first segment and 2b + 1 for its last, and page_combine_kernel joins
+// the parts. With many tiles, or short ones, every CTA takes whole tiles
+// instead.
+struct Share {
+  long long line;   // units of a kv head
+  long long tiles;  // tiles of a kv head
+  long long ctas;   // B
+  bool whole;       // a tile a CTA
+  __device__ __forceinline__ long long start(const PageAttnArgs& a, long long b) const {
+    return whole ? b : line * a.c.nkv * b / ctas;
+  }
+};
+struct Segment {
+  int h, s, tile;  // kv head, stream, tile of it
+  int u, x0, x1;   // units of the tile, and the part of them
 };
 
-// Find item `want` of a call (split_only: tile `want` among the tiles of the
-// streams with ns > 1). One warp; every lane gets the answer. Returns false
-// past the last one.
-__device__ __forceinline__ bool find_item(const PageAttnArgs& a, int want, bool split_only, Item* out) {
+__device__ __forceinline__ int stream_units(const PageAttnArgs& a, int s, int* mt, bool flag) {
+  bool bad;
+  const StreamRows q = stream_rows(a.r, s, &bad);
+  if (bad && flag) flag_status(a.r.status, DFLASH_STATUS_BAD_ROWS);
+  *mt = static_cast<int>((static_cast<int64_t>(q.n) * a.G + a.tile - 1) / a.tile);
+  if (q.n == 0) return 0;
+  const int lo = a.window > 0 ? max(0, q.C - a.window + 1) : 0;
+  return unit_range(lo, q.C + q.n, a.sinks, a.unit).n;
+}
+
+// One warp; every lane gets the answer.
+__device__ __forceinline__ Share share_of(const PageAttnArgs& a) {
   const int lane = threadIdx.x & 31;
-  auto units_of = [&](int s, int* mt) -> int {
-    bool bad;
-    const StreamRows q = stream_rows(a.r, s, &bad);
-    if (bad && blockIdx.x == 0 && blockIdx.y == 0) flag_status(a.r.status, DFLASH_STATUS_BAD_ROWS);
-    *mt = static_cast<int>((static_cast<int64_t>(q.n) * a.G + a.tile - 1) / a.tile);
-    if (q.n == 0) return 0;
-    const int lo = a.window > 0 ? max(0, q.C - a.window + 1) : 0;
-    return unit_range(lo, q.C + q.n, a.sinks, a.unit).n;
-  };
-  // total units over the tiles of all streams
-  long long total = 0;
-  int mt0 = 0, u0 = 0;
+  long long line = 0, tiles = 0;
+  int most = 0;
   for (int s0 = 0; s0 < a.r.S; s0 += 32) {
     int mt = 0, u = 0;
-    if (s0 + lane < a.r.S) u = units_of(s0 + lane, &mt);
-    if (s0 == 0) {
-      mt0 = mt;
-      u0 = u;
-    }
-    total += static_cast<long long>(mt) * u;
+    if (s0 + lane < a.r.S) u = stream_units(a, s0 + lane, &mt, blockIdx.x == 0 && blockIdx.y == 0);
+    line += static_cast<long long>(mt) * u;
+    tiles += mt;
+    most = max(most, u);
   }
-  for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  const long long per = (total * a.c.nkv + a.target - 1) / a.target;
-  const int upi = static_cast<int>(per > a.min_units ? (per < 0x7fffffffll ? per : 0x7fffffffll) : a.min_units);
-  int base = 0, slots = 0;
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) {
+    line += __shfl_xor_sync(0xffffffffu, line, o);
+    tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  Share sh;
+  sh.line = line;
+  sh.tiles = tiles;
+  sh.whole = a.part_o == nullptr || most <= a.no_split || tiles * a.c.nkv >= 3ll * a.target;
+  if (sh.whole) {
+    sh.ctas = tiles * a.c.nkv;
+  } else {
+    const long long b = (line * a.c.nkv + a.min_units - 1) / a.min_units;
+    sh.ctas = b < a.target ? b : a.target;
+  }
+  return sh;
+}
+
+// The segment at place `at` of the line (whole: tile `at`), open to the tile's
+// end. One warp.
+__device__ __forceinline__ Segment segment_at(const PageAttnArgs& a, const Share& sh, long long at) {
+  const int lane = threadIdx.x & 31;
+  const long long per = sh.whole ? sh.tiles : sh.line;
+  Segment g;
+  g.h = static_cast<int>(at / per);
+  const long long r = at - g.h * per;
+  long long base = 0;
+  g.s = g.tile = g.u = g.x0 = g.x1 = 0;
   for (int s0 = 0; s0 < a.r.S; s0 += 32) {
-    int mt = mt0, u = u0;
-    if (s0 > 0) {
-      mt = u = 0;
-      if (s0 + lane < a.r.S) u = units_of(s0 + lane, &mt);
-    }
-    // a stream whose rows see no slot still has its output written
-    const int ns = u > 0 ? static_cast<int>((static_cast<long long>(u) + upi - 1) / upi) : 1;
-    const int cnt = split_only ? (ns > 1 ? mt : 0) : mt * ns;
-    const int part = ns > 1 ? mt * ns : 0;
-    int ic = cnt, ip = part;
+    int mt = 0, u = 0;
+    if (s0 + lane < a.r.S) u = stream_units(a, s0 + lane, &mt, false);
+    const long long cnt = sh.whole ? mt : static_cast<long long>(mt) * u;
+    long long inc = cnt;
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, ic, o), y = __shfl_up_sync(0xffffffffu, ip, o);
-      if (lane >= o) {
-        ic += x;
-        ip += y;
-      }
+      const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, want < base + ic);
+    const unsigned hit = __ballot_sync(0xffffffffu, r < base + inc);
     if (hit) {
       const int l = __ffs(hit) - 1;
-      const int before = base + __shfl_sync(0xffffffffu, ic - cnt, l);
-      const int nsl = __shfl_sync(0xffffffffu, ns, l);
-      const int slot0 = slots + __shfl_sync(0xffffffffu, ip - part, l);
-      const int rel = want - before, tiles = __shfl_sync(0xffffffffu, mt, l);
-      const int tile = split_only ? rel : rel / nsl;
-      out->s = s0 + l;
-      out->ns = nsl;
-      out->tile = tiles - 1 - tile;  // the last rows see most: their items start first
-      out->split = split_only ? 0 : rel - tile * nsl;
-      out->slot = slot0 + tile * nsl + out->split;
-      return true;
+      const long long rel = r - base - __shfl_sync(0xffffffffu, inc - cnt, l);
+      g.s = s0 + l;
+      g.u = __shfl_sync(0xffffffffu, u, l);
+      const int tiles = __shfl_sync(0xffffffffu, mt, l);
+      const int tile = static_cast<int>(sh.whole ? rel : rel / g.u);
+      g.x0 = sh.whole ? 0 : static_cast<int>(rel - static_cast<long long>(tile) * g.u);
+      g.x1 = g.u;
+      g.tile = tiles - 1 - tile;  // the last rows see most: whole tiles start with them
+      return g;
     }
-    base += __shfl_sync(0xffffffffu, ic, 31);
-    slots += __shfl_sync(0xffffffffu, ip, 31);
+    base += __shfl_sync(0xffffffffu, inc, 31);
   }
-  return false;
+  return g;
+}
+
+// A CTA's run of segments, kept in shared memory between them.
+struct Run {
+  Share sh;
+  long long at, end;
+  Segment seg;
+  int left;  // whether seg is one
+};
+__device__ __forceinline__ void run_begin(const PageAttnArgs& a, Run* run) {
+  const Share sh = share_of(a);
+  if ((threadIdx.x & 31) == 0) {
+    const bool on = blockIdx.x < sh.ctas;
+    run->sh = sh;
+    run->at = on ? sh.start(a, blockIdx.x) : 0;
+    run->end = on ? sh.start(a, blockIdx.x + 1ll) : 0;
+  }
+  __syncwarp();
+}
+__device__ __forceinline__ void run_next(const PageAttnArgs& a, Run* run) {
+  const long long at = run->at, left = run->end - at;
+  Segment sg{};
+  if (left > 0) {
+    const Share sh = run->sh;
+    sg = segment_at(a, sh, at);
+    if (!sh.whole && sg.x1 - sg.x0 > left) sg.x1 = sg.x0 + static_cast<int>(left);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) run->at = at + (sh.whole ? 1 : sg.x1 - sg.x0);
+  }
+  if ((threadIdx.x & 31) == 0) {
+    run->seg = sg;
+    run->left = left > 0;
+  }
+  __syncwarp();
 }
 
 // What one (query row, head) pair of a tile sees.
@@ -189,9 +248,10 @@ int launch_page_read(const PagesArgs& c, const RowsArgs& r, __nv_bfloat16* k, in
                      int64_t v_ld, bool fp4, cudaStream_t st);
 // Work split of a call (host side): which kernel, its tile and its workspace.
 struct PagePlan {
-  bool tc;
-  int tile, unit, target, min_units, slots;
-  int64_t items, split_tiles;
+  bool tc;      // the tensor-memory kernel
+  bool split;   // tiles may be split: a workspace and a combine launch
+  int tile, unit, target, min_units, no_split;
+  int64_t ctas;
 };
 PagePlan page_attention_plan(const dflash_pages& c, const dflash_rows& r, int nq);
 int launch_page_attention(const PageAttnArgs& a, const PagePlan& p, bool fp4, cudaStream_t st);

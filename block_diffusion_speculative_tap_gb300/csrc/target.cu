@@ -78,16 +78,15 @@ bool good_rows(const void* p, int64_t ld, int64_t heads, int d) {
 }
 
 size_t attention_ws(const PagePlan& p, const dflash_pages& c) {
-  const size_t rows = static_cast<size_t>(p.slots) * c.n_kv_heads * p.tile;
-  return (rows * c.head_dim + rows * 2) * sizeof(float);
+  return p.split ? static_cast<size_t>(2 * p.target) * p.tile * (c.head_dim + 2) * sizeof(float) : 0;
 }
 
 int check_heads(const dflash_pages* c, int nq) {
   return nq < 1 || nq % c->n_kv_heads || nq / c->n_kv_heads > DFLASH_MAX_PAGE_GROUP ? DFLASH_E_SHAPE : DFLASH_OK;
 }
 
-// the grid's x axis holds the call's items
-int check_items(const PagePlan& p) { return p.items > 0x7fffffff ? DFLASH_E_SHAPE : DFLASH_OK; }
+// the grid's x axis holds the call's CTAs
+int check_ctas(const PagePlan& p) { return p.ctas > 0x7fffffff ? DFLASH_E_SHAPE : DFLASH_OK; }
 
 }  // namespace
 
@@ -136,7 +135,7 @@ int dflash_page_attention_workspace_bytes(const dflash_pages* c, const dflash_ro
   *bytes = 0;
   if (nothing(c, r)) return DFLASH_OK;
   const PagePlan p = page_attention_plan(*c, *r, n_q_heads);
-  rc = check_items(p);
+  rc = check_ctas(p);
   if (!rc) *bytes = attention_ws(p, *c);
   return rc;
 }
@@ -159,7 +158,7 @@ int dflash_page_attention(const dflash_pages* c, const dflash_rows* r, int n_q_h
   if (!good_rows(q, q_ld, n_q_heads, c->head_dim) || !good_rows(out, out_ld, n_q_heads, c->head_dim))
     return DFLASH_E_INVALID_ARG;
   const PagePlan p = page_attention_plan(*c, *r, n_q_heads);
-  rc = check_items(p);
+  rc = check_ctas(p);
   if (rc) return rc;
   const size_t need = attention_ws(p, *c);
   if (need > 0 && (!ws || ws_bytes < need || !aligned(ws, 16))) return DFLASH_E_WORKSPACE;
@@ -182,9 +181,9 @@ int dflash_page_attention(const dflash_pages* c, const dflash_rows* r, int n_q_h
   a.tile = p.tile;
   a.target = p.target;
   a.min_units = p.min_units;
-  a.slots = p.slots;
-  a.part_o = static_cast<float*>(ws);
-  a.part_ml = a.part_o ? a.part_o + static_cast<size_t>(p.slots) * c->n_kv_heads * p.tile * c->head_dim : nullptr;
+  a.no_split = p.no_split;
+  a.part_o = p.split ? static_cast<float*>(ws) : nullptr;
+  a.part_ml = p.split ? a.part_o + static_cast<size_t>(2 * p.target) * p.tile * c->head_dim : nullptr;
   return launch_page_attention(a, p, c->format == DFLASH_PAGES_FP4, reinterpret_cast<cudaStream_t>(stream));
 }
 
