@@ -12,10 +12,12 @@
 // in fp32, every operation rounded, the result rounded once to bf16.
 //
 // logit_rules_kernel: one CTA takes a slice of 2048 tokens of a stream for a
-// group of its rows; a thread keeps its 8 tokens' counts and biases in
-// registers and streams the rows: 16 bytes of scores in, one byte of the
-// mask, 16 bytes out. The drafted tokens and biases that fall into the slice
-// (few) wait in shared memory. Bound by the scores' bytes.
+// group of its rows. The tokens of the slice that any rule touches (a count, a
+// bias, a drafted node: a few in a thousand) are listed in shared memory; the
+// rows are copied under the mask, 16 bytes of scores and a byte of the mask a
+// thread, and then the listed scores are edited in place, a thread each: with
+// the edits inside the copy nearly every warp had some thread to wait for
+// (32 trees of 93 nodes x 151936: 668 us). Bound by the scores' bytes.
 //
 // token_counts_kernel: adds tokens to a stream's counts, one thread a token;
 // equal tokens of a warp go in one update, which saturates at 32767.
@@ -36,13 +38,18 @@ __device__ __forceinline__ float penalise(float x, int count, bool prompt, float
   return x;
 }
 
-__global__ void __launch_bounds__(kThreads) logit_rules_kernel(const RulesArgs a) {
-  __shared__ float bias[kSlice];
+// Rows a thread has in flight: 16 bytes of scores and a byte of the mask each.
+constexpr int kBatch = 4;
+
+__global__ void __launch_bounds__(kThreads, 4) logit_rules_kernel(const RulesArgs a) {
+  __shared__ __align__(16) float bias[kSlice];
   __shared__ uint32_t path[DFLASH_MAX_TREE_NODES];  // node << 16 | token of the slice
-  __shared__ int n_path;
+  __shared__ uint32_t marked[kSlice / 32];          // tokens of the slice with a count, a bias or a drafted node
+  __shared__ uint16_t list[kSlice];
+  __shared__ int n_path, n_list;
   __shared__ uint16_t bid[kThreads];
   __shared__ float bval[kThreads];
-  __shared__ int wcount[kThreads / 32 + 1];
+  __shared__ int wcount[kThreads / 32];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -50,106 +57,140 @@ __global__ void __launch_bounds__(kThreads) logit_rules_kernel(const RulesArgs a
   const int n0 = blockIdx.y * a.group, n1 = min(a.N, n0 + a.group);
   const bool on = v < a.V;
   for (int s = blockIdx.z; s < a.S; s += gridDim.z) {
-    if (tid == 0) n_path = 0;
-    bool any_bias = false;
-    float b[8] = {};
+    const int64_t row0 = static_cast<int64_t>(s) * a.N;
+    const __nv_bfloat16* in = a.in + row0 * a.V + v;
+    __nv_bfloat16* out = a.out + row0 * a.V + v;
+    const uint8_t* gram = a.grammar ? reinterpret_cast<const uint8_t*>(a.grammar + row0 * a.words) + (v >> 3) : nullptr;
+    uint4 x[kBatch];
+    unsigned may[kBatch];
+    auto fetch = [&](int n) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        may[i] = 0xffu;
+        if (on && n + i < n1) {
+          x[i] = *reinterpret_cast<const uint4*>(in + static_cast<int64_t>(n + i) * a.V);
+          if (gram) may[i] = gram[static_cast<int64_t>(n + i) * a.words * 4];
+        }
+      }
+    };
+    fetch(n0);
+    // ------------------------------------------------ what the rules touch in the slice
     uint4 cw = make_uint4(0u, 0u, 0u, 0u);
     if (a.counts && on) cw = *reinterpret_cast<const uint4*>(a.counts + static_cast<int64_t>(s) * a.V + v);
+    int e0 = 0, e1 = 0;
+    if (a.bias_start) {
+      e0 = max(0, min(a.bias_start[s], a.n_bias));
+      e1 = max(e0, min(a.bias_start[s + 1], a.n_bias));
+    }
+    if (tid == 0) n_path = n_list = 0;
+    {
+      const uint32_t c4[4] = {cw.x, cw.y, cw.z, cw.w};
+      unsigned mine = 0u;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mine |= ((c4[k >> 1] >> (16 * (k & 1))) & 0xffffu) != 0u ? 1u << k : 0u;
+      reinterpret_cast<uint8_t*>(marked)[tid] = static_cast<uint8_t>(mine);
+    }
+    if (e1 > e0) {
+      *reinterpret_cast<float4*>(bias + tid * 8) = make_float4(0.f, 0.f, 0.f, 0.f);
+      *reinterpret_cast<float4*>(bias + tid * 8 + 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     __syncthreads();
-    // the drafted tokens of the slice; the root's (node 0) are in the counts
+    // drafted tokens; the root's (node 0) are in the counts
     if (a.tokens)
       for (int m = 1 + tid; m < a.N; m += kThreads) {
-        const int id = a.tokens[static_cast<int64_t>(s) * a.N + m];
-        if (id >= v0 && id < v0 + kSlice && id < a.V)
+        const int id = a.tokens[row0 + m];
+        if (id >= v0 && id < v0 + kSlice && id < a.V) {
           path[atomicAdd(&n_path, 1)] = static_cast<uint32_t>(m) << 16 | static_cast<uint32_t>(id - v0);
+          atomicOr(&marked[(id - v0) >> 5], 1u << ((id - v0) & 31));
+        }
       }
-    // the biases of the slice, in list order: equal ids add up in that order
-    if (a.bias_start) {
-      const int e0 = max(0, min(a.bias_start[s], a.n_bias)), e1 = max(e0, min(a.bias_start[s + 1], a.n_bias));
-      if (e1 > e0) {
-        for (int i = tid; i < kSlice; i += kThreads) bias[i] = 0.f;
-        for (int e = e0; e < e1; e += kThreads) {
-          __syncthreads();
-          const int id = e + tid < e1 ? a.bias_ids[e + tid] : -1;
-          const bool in = id >= v0 && id < v0 + kSlice && id < a.V;
-          const unsigned w = __ballot_sync(0xffffffffu, in);
-          if (lane == 0) wcount[warp] = __popc(w);
-          __syncthreads();
-          int at = __popc(w & ((1u << lane) - 1u)), total = 0;
-          for (int k = 0; k < kThreads / 32; ++k) {
-            if (k < warp) at += wcount[k];
-            total += wcount[k];
-          }
-          if (total == 0) continue;
-          any_bias = true;
-          if (in) {
-            bid[at] = static_cast<uint16_t>(id - v0);
-            bval[at] = a.bias_vals[e + tid];
-          }
-          __syncthreads();
-          if (tid < total) {
-            bool first = true;
-            for (int k = 0; k < tid; ++k) first &= bid[k] != bid[tid];
-            if (first) {
-              float sum = bias[bid[tid]];
-              for (int k = tid; k < total; ++k)
-                if (bid[k] == bid[tid]) sum = __fadd_rn(sum, bval[k]);
-              bias[bid[tid]] = sum;
-            }
+    // biases, in list order: equal ids add up in that order
+    for (int e = e0; e < e1; e += kThreads) {
+      const int id = e + tid < e1 ? a.bias_ids[e + tid] : -1;
+      const bool in_slice = id >= v0 && id < v0 + kSlice && id < a.V;
+      const unsigned w = __ballot_sync(0xffffffffu, in_slice);
+      if (lane == 0) wcount[warp] = __popc(w);
+      if (__syncthreads_or(in_slice)) {
+        int at = __popc(w & ((1u << lane) - 1u)), total = 0;
+        for (int k = 0; k < kThreads / 32; ++k) {
+          if (k < warp) at += wcount[k];
+          total += wcount[k];
+        }
+        if (in_slice) {
+          bid[at] = static_cast<uint16_t>(id - v0);
+          bval[at] = a.bias_vals[e + tid];
+          atomicOr(&marked[(id - v0) >> 5], 1u << ((id - v0) & 31));
+        }
+        __syncthreads();
+        if (tid < total) {
+          bool first = true;
+          for (int k = 0; k < tid; ++k) first &= bid[k] != bid[tid];
+          if (first) {
+            float sum = bias[bid[tid]];
+            for (int k = tid; k < total; ++k)
+              if (bid[k] == bid[tid]) sum = __fadd_rn(sum, bval[k]);
+            bias[bid[tid]] = sum;
           }
         }
+      }
+      __syncthreads();  // the lists are written again
+    }
+    __syncthreads();
+    {
+      unsigned mine = reinterpret_cast<const uint8_t*>(marked)[tid];
+      if (mine) {
+        int at = atomicAdd(&n_list, __popc(mine));
+        for (; mine; mine &= mine - 1u) list[at++] = static_cast<uint16_t>(tid * 8 + __ffs(mine) - 1);
+      }
+    }
+    // ------------------------------------------------ every score: copied, or -inf by the mask
+    for (int n = n0; n < n1; n += kBatch) {
+      uint4 y[kBatch];
+      unsigned allow[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        y[i] = x[i];
+        allow[i] = may[i];
+      }
+      fetch(n + kBatch);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        uint32_t w[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          // two bits of the mask to two halves
+          const uint32_t two = (allow[i] >> (2 * k)) & 3u;
+          const uint32_t keep = ((two & 1u) | ((two & 2u) << 15)) * 0xffffu;
+          w[k] = (w[k] & keep) | (0xff80ff80u & ~keep);
+        }
+        if (on && n + i < n1)
+          *reinterpret_cast<uint4*>(out + static_cast<int64_t>(n + i) * a.V) = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
     __syncthreads();
-    if (any_bias)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) b[k] = bias[tid * 8 + k];
-    const float rep = a.repetition ? a.repetition[s] : 1.f;
-    const float freq = a.frequency ? a.frequency[s] : 0.f;
-    const float pres = a.presence ? a.presence[s] : 0.f;
-    const int np = n_path;
-    const bool counted = (cw.x | cw.y | cw.z | cw.w) != 0u;
-    const uint32_t c4[4] = {cw.x, cw.y, cw.z, cw.w};
-    if (on) {
-#pragma unroll 4
-      for (int n = n0; n < n1; ++n) {
-        const int64_t row = static_cast<int64_t>(s) * a.N + n;
-        const uint4 xw = *reinterpret_cast<const uint4*>(a.in + row * a.V + v);
-        unsigned may = 0xffu;
-        if (a.grammar) may = reinterpret_cast<const uint8_t*>(a.grammar + row * a.words)[v >> 3];
-        uint32_t w[4] = {xw.x, xw.y, xw.z, xw.w};
-        unsigned extra[8];
-        bool drafted = false;
-        if (np > 0) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) extra[k] = 0u;
-          for (int p = 0; p < np; ++p) {
-            const int m = path[p] >> 16, k0 = static_cast<int>(path[p] & 0xffffu) - tid * 8;
-            if (k0 < 0 || k0 >= 8) continue;
-            const bool hit = a.node_mask ? (a.node_mask[row * a.mask_ld + (m >> 5)] >> (m & 31)) & 1u : m <= n;
-            if (!hit) continue;
-            drafted = true;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) extra[k] += k == k0;
-          }
+    // ------------------------------------------------ the few that a rule touches, again
+    const int nl = n_list, np = n_path, rows = n1 - n0;
+    if (nl > 0) {
+      const float rep = a.repetition ? a.repetition[s] : 1.f;
+      const float freq = a.frequency ? a.frequency[s] : 0.f;
+      const float pres = a.presence ? a.presence[s] : 0.f;
+      for (int i = tid; i < nl * rows; i += kThreads) {
+        const int n = n0 + i / nl, id = list[i % nl];
+        if (a.grammar) {
+          const uint32_t word = a.grammar[(row0 + n) * a.words + ((v0 + id) >> 5)];
+          if (!((word >> ((v0 + id) & 31)) & 1u)) continue;
         }
-        if (counted || drafted || any_bias) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            float x = __uint_as_float((k & 1) ? w[k >> 1] & 0xffff0000u : w[k >> 1] << 16);
-            const unsigned c = (c4[k >> 1] >> (16 * (k & 1))) & 0xffffu;
-            x = penalise(x, static_cast<int>((c & 0x7fffu) + (drafted ? extra[k] : 0u)), c >> 15, rep, freq, pres);
-            x = __fadd_rn(x, b[k]);
-            const uint32_t h = __bfloat16_as_ushort(__float2bfloat16_rn(x));
-            w[k >> 1] = (k & 1) ? (w[k >> 1] & 0xffffu) | (h << 16) : (w[k >> 1] & 0xffff0000u) | h;
-          }
+        const unsigned c = a.counts ? a.counts[static_cast<int64_t>(s) * a.V + v0 + id] : 0u;
+        int count = static_cast<int>(c & 0x7fffu);
+        for (int p = 0; p < np; ++p) {
+          const int m = path[p] >> 16;
+          if (static_cast<int>(path[p] & 0xffffu) != id) continue;
+          count += a.node_mask ? (a.node_mask[(row0 + n) * a.mask_ld + (m >> 5)] >> (m & 31)) & 1u : m <= n;
         }
-        if (may != 0xffu) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (!((may >> k) & 1u)) w[k >> 1] = (k & 1) ? (w[k >> 1] & 0xffffu) | 0xff800000u : (w[k >> 1] & 0xffff0000u) | 0xff80u;
-        }
-        *reinterpret_cast<uint4*>(a.out + row * a.V + v) = make_uint4(w[0], w[1], w[2], w[3]);
+        __nv_bfloat16* at = a.out + (row0 + n) * a.V + v0 + id;
+        float f = penalise(__bfloat162float(*at), count, c >> 15, rep, freq, pres);
+        if (e1 > e0) f = __fadd_rn(f, bias[id]);
+        *at = __float2bfloat16_rn(f);
       }
     }
     __syncthreads();  // the next stream writes the shared lists
@@ -204,11 +245,13 @@ __global__ void __launch_bounds__(256) token_counts_kernel(uint16_t* counts, con
 int launch_logit_rules(const RulesArgs& args, int num_sms, cudaStream_t st) {
   RulesArgs a = args;
   const int slices = (a.V + kSlice - 1) / kSlice;
-  // rows a CTA: its counts, biases and drafted tokens are read once for all
-  // of them, so as many as leave about four CTAs an SM
+  // rows a CTA: its counts, biases and drafted tokens are looked up once for
+  // all of them, so as many as leave two waves of four CTAs an SM, and whole
+  // batches of rows in flight
   const int64_t rows_all = static_cast<int64_t>(a.S) * a.N * slices;
-  int64_t group = rows_all / (4ll * num_sms);
-  a.group = static_cast<int>(group < 1 ? 1 : group > a.N ? a.N : group);
+  int64_t group = rows_all / (8ll * num_sms);
+  group = (group + kBatch - 1) / kBatch * kBatch;
+  a.group = static_cast<int>(group < kBatch ? kBatch : group > a.N ? a.N : group);
   const int groups = (a.N + a.group - 1) / a.group;
   TraceScope ts(st, "logit_rules", static_cast<double>(a.S) * a.V * (4.0 * a.N + (a.counts ? 2.0 : 0.0) +
                                    (a.grammar ? a.N / 8.0 : 0.0)), 0.0);

@@ -26,22 +26,18 @@ def _need(t, dtype, dev, what):
     return t.data_ptr()
 
 
-def _on(dev):
-    """The current stream of the tensors' device, which has to be the current one."""
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {dev}: expected the current CUDA device")
-    return torch.cuda.current_stream().cuda_stream
+def _on(index):
+    """The current stream of a device (by index), which has to be the current one."""
+    if index < 0 or index != torch.cuda.current_device():
+        raise ValueError("expected tensors on the current CUDA device")
+    return torch._C._cuda_getCurrentRawStream(index)  # the handle without a Stream object (3 us)
 
 
-def _heads(t, dtype, dev, dim, what):
-    """(pointer, row stride, heads) of rows [T, heads, dim] whose heads are dense."""
-    if t.dtype != dtype or t.device != dev or t.dim() != 3 or t.shape[2] != dim:
-        raise ValueError(f"{what}: expected {dtype} [rows, heads, {dim}] on {dev}")
-    T, h, _ = t.shape
-    st = t.stride()
-    if st[2] != 1 or (h > 1 and st[1] != dim):
-        raise ValueError(f"{what}: the heads of a row must be dense")
-    return t.data_ptr(), (st[0] if T > 1 else h * dim), h
+
+
+def _like(t):
+    """A dense tensor of t's shape and type (t may be strided)."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 class Rows:
@@ -53,7 +49,7 @@ class Rows:
 
     def __init__(self, row_start, lens, rows: int, max_rows: int, depth=None):
         dev = row_start.device
-        self.device = dev
+        self.device, self.index = dev, row_start.get_device()
         self.streams = lens.numel()
         if row_start.numel() != self.streams + 1:
             raise ValueError("row_start: one entry more than lens")
@@ -86,7 +82,8 @@ class PagedCache:
         n, h, page, row = k.shape
         d = row * 2 if self.fp4 else row
         self.k, self.v, self.table, self.k_scale, self.v_scale, self.status = k, v, table, k_scale, v_scale, status
-        self.device, self.streams, self.n_kv, self.head_dim = dev, table.shape[0], h, d
+        self.device, self.index = dev, k.get_device()
+        self.streams, self.n_kv, self.head_dim = table.shape[0], h, d
         if self.fp4:
             for s in (k_scale, v_scale):
                 if s is None or tuple(s.shape) != (n, h, page, d // 16):
@@ -100,17 +97,26 @@ class PagedCache:
         )
         self._ref = C.byref(self.desc)
         self._status = _need(status, torch.int32, dev, "status") if status is not None else None
+        self._ws_bytes = {}  # prices by (rows, max_rows, heads)
+        self._scale = 1.0 / math.sqrt(d)
 
     def _check(self, rows):
-        if rows.device != self.device or rows.streams != self.streams:
+        if rows.index != self.index or rows.streams != self.streams:
             raise ValueError("rows: another device, or another number of streams than the table's")
-        return _on(self.device)
+        return _on(self.index)
 
     def _rows_of(self, t, rows, what, n=None):
-        p, ld, h = _heads(t, torch.bfloat16, self.device, self.head_dim, what)
-        if t.shape[0] < rows.rows or (n is not None and h != n):
-            raise ValueError(f"{what}: {rows.rows} rows of {n if n is not None else h} heads")
-        return p, ld, h
+        """(pointer, row stride, heads) of bf16 rows [>= rows, heads, d] whose heads are dense."""
+        shape, st = t.shape, t.stride()
+        d = self.head_dim
+        if t.dtype != torch.bfloat16 or t.get_device() != self.index or len(shape) != 3 or shape[2] != d:
+            raise ValueError(f"{what}: expected torch.bfloat16 [rows, heads, {d}] on {self.device}")
+        T, h = shape[0], shape[1]
+        if T < rows.rows or (n is not None and h != n):
+            raise ValueError(f"{what}: expected {rows.rows} rows of {n if n is not None else h} heads")
+        if st[2] != 1 or (h > 1 and st[1] != d):
+            raise ValueError(f"{what}: the heads of a row must be dense")
+        return t.data_ptr(), (st[0] if T > 1 else h * d), h
 
     def append(self, rows: Rows, k, v, rope=None, q=None, q_out=None):
         """dflash_page_append: k, v bf16 [rows, n_kv, d] go to the rows' slots, keys
@@ -129,8 +135,10 @@ class PagedCache:
         if q is not None:
             qp, ql, nq = self._rows_of(q, rows, "q")
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            op, ol, _ = self._rows_of(q_out, rows, "q_out", nq)
+                q_out = _like(q)
+                op, ol = q_out.data_ptr(), nq * self.head_dim
+            else:
+                op, ol, _ = self._rows_of(q_out, rows, "q_out", nq)
         elif q_out is not None:
             raise ValueError("q_out without q")
         check(
@@ -152,10 +160,14 @@ class PagedCache:
         return k, v
 
     def workspace_bytes(self, rows: Rows, n_q: int) -> int:
-        nb = C.c_size_t()
-        check(lib.dflash_page_attention_workspace_bytes(self._ref, rows._ref, n_q, C.byref(nb)),
-              "dflash_page_attention_workspace_bytes")
-        return nb.value
+        key = (rows.rows, rows.max_rows, n_q)
+        nbytes = self._ws_bytes.get(key)
+        if nbytes is None:
+            nb = C.c_size_t()
+            check(lib.dflash_page_attention_workspace_bytes(self._ref, rows._ref, n_q, C.byref(nb)),
+                  "dflash_page_attention_workspace_bytes")
+            nbytes = self._ws_bytes[key] = nb.value
+        return nbytes
 
     def attend(self, rows: Rows, q, window=0, sinks=0, mask="causal", scale=None, out=None, ws=None):
         """dflash_page_attention of q bf16 [rows, n_q, d]. mask: "causal", "block", or
@@ -174,16 +186,20 @@ class PagedCache:
                 raise ValueError("mask: int32 [rows, words]")
             mp, mld = _need(mask, torch.int32, self.device, "mask"), mask.shape[1]
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        op, ol, _ = self._rows_of(out, rows, "out", nq)
+            out = _like(q)
+            op, ol = out.data_ptr(), nq * self.head_dim
+        else:
+            op, ol, _ = self._rows_of(out, rows, "out", nq)
         if ws is None:
             nbytes = self.workspace_bytes(rows, nq)
             ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device) if nbytes else None
-        wp, wn = (_need(ws, torch.uint8, self.device, "ws"), ws.numel()) if ws is not None else (None, 0)
+            wp, wn = (ws.data_ptr(), nbytes) if nbytes else (None, 0)
+        else:
+            wp, wn = _need(ws, torch.uint8, self.device, "ws"), ws.numel()
         check(
             lib.dflash_page_attention(
-                self._ref, rows._ref, nq, qp, ql, scale if scale is not None else 1.0 / math.sqrt(self.head_dim),
-                window, sinks, mode, mp, mld, op, ol, self._status, wp, wn, stream,
+                self._ref, rows._ref, nq, qp, ql, self._scale if scale is None else scale, window, sinks, mode, mp, mld,
+                op, ol, self._status, wp, wn, stream,
             ),
             "dflash_page_attention",
         )
@@ -195,7 +211,7 @@ def token_counts(counts, tokens, row_start=None, prompt=False):
     0..14 output count). tokens: int32, ragged with row_start int32 [S + 1], or
     [S, n] (verify's out_tokens as they are: -1s are skipped). Returns counts."""
     dev = counts.device
-    stream = _on(dev)
+    stream = _on(counts.get_device())
     S, V = counts.shape
     total, per = tokens.numel(), 0
     if row_start is None:
@@ -223,12 +239,12 @@ def logit_rules(logits, counts=None, tokens=None, node_mask=None, repetition=Non
     [S + 1], ids int32, values fp32); grammar int32 [S, rows, ceil(V / 32)].
     Returns out (a new tensor unless given; out may be logits)."""
     dev = logits.device
-    stream = _on(dev)
+    stream = _on(logits.get_device())
     if logits.dim() != 3:
         raise ValueError("logits: [S, rows, V]")
     S, N, V = logits.shape
     if out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+        out = _like(logits)
 
     def opt(t, dtype, shape, what):
         if t is None:
