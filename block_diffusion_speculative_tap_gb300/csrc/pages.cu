@@ -7,11 +7,11 @@
 // the row's slot of its stream's pages: as bf16, or as 4-bit codes with one
 // scale a group of 16 dims,
 //   s = e4m3(max|y| / 6),  code_i = e2m1(y_i / s)   (both to nearest, ties to
-// even; the quantised value is the bf16 one). A thread takes 16 dims of the
-// lower half and the 16 they pair with, two whole groups, so neither the
-// rotation nor a group's maximum leaves it. Bound by the rows' bytes: each is
-// read and written once. The row's stream is found by one load a lane over
-// row_start, and the values are loaded before anything depends on it.
+// even; the quantised value is the bf16 one). A thread takes 8 dims of the
+// lower half and the 8 they pair with (16-byte pieces, whole sectors a warp; a
+// group's maximum is shared with the neighbouring lane) of up to four heads at
+// a time, under one load of the angles, and loads them before the row's place
+// is looked up. Bound by the rows' bytes: each is read and written once.
 //
 // page_read_kernel: the rows' values back, as bf16 (a 4-bit value times its
 // e4m3 scale has at most six significant bits: exact in bf16).
@@ -25,90 +25,73 @@ namespace dfl {
 
 namespace {
 
-constexpr int kAppendThreads = 128;
-
-// The stream that holds row `t` (row_start[s] <= t < row_start[s + 1]): the
-// number of streams that end at or before t. One warp; S when there is none.
-__device__ __forceinline__ int find_stream(const RowsArgs& r, int t) {
-  const int lane = threadIdx.x & 31;
-  for (int s0 = 0; s0 < r.S; s0 += 32) {
-    const bool past = s0 + lane >= r.S || r.row_start[s0 + lane + 1] > t;
-    const unsigned hit = __ballot_sync(0xffffffffu, past);
-    if (hit) return min(r.S, s0 + __ffs(hit) - 1);
-  }
-  return r.S;
-}
+constexpr int kThreads = 128;
 
 struct Place {
   int pos;      // -1: no such row, leave everything as it is
   int64_t row;  // (page * nkv) * page_size + slot of kv head 0, -1: no slot
 };
 
+// Where row `t` goes. Every warp looks the streams up for itself, a lane a
+// stream: the row's is the first that ends past t.
 __device__ __forceinline__ Place find_place(const PagesArgs& c, const RowsArgs& r, int t) {
   Place p{-1, -1};
-  const int s = find_stream(r, t);
-  if (s >= r.S) return p;
-  bool bad;
-  const StreamRows q = stream_rows(r, s, &bad);
-  const int j = t - q.row0;
-  if (bad) flag_status(r.status, DFLASH_STATUS_BAD_ROWS);
-  if (j < 0 || j >= q.n) return p;
-  p.pos = q.C + j;
-  if (r.depth) {
-    const int d = r.depth[t];
-    if (d < 0 || d > 0x3fffffff) {
+  const int lane = threadIdx.x & 31;
+  const int depth = r.depth ? r.depth[t] : 0;
+  for (int s0 = 0; s0 < r.S; s0 += 32) {
+    const int s = min(s0 + lane, r.S - 1);
+    bool bad;
+    const StreamRows mine = stream_rows(r, s, &bad);
+    const unsigned past = __ballot_sync(0xffffffffu, s0 + lane < r.S && r.row_start[s + 1] > t);
+    if (!past) continue;
+    const int l = __ffs(past) - 1, sx = s0 + l;
+    if (__shfl_sync(0xffffffffu, bad, l)) flag_status(r.status, DFLASH_STATUS_BAD_ROWS);
+    const int j = t - __shfl_sync(0xffffffffu, mine.row0, l);
+    const int n = __shfl_sync(0xffffffffu, mine.n, l), C = __shfl_sync(0xffffffffu, mine.C, l);
+    if (j < 0 || j >= n) return p;
+    if (depth < 0 || depth > 0x3fffffff) {
       flag_status(r.status, DFLASH_STATUS_BAD_ROWS);
-      p.pos = -1;
       return p;
     }
-    p.pos = q.C + d;
+    p.pos = C + (r.depth ? depth : j);
+    const int slot = C + j, col = slot >> c.page_log2;
+    const int pg = col < c.cols ? c.table[static_cast<int64_t>(sx) * c.cols + col] : -1;
+    if (pg >= 0 && pg < c.n_pages)
+      p.row = static_cast<int64_t>(pg) * c.nkv * c.page + (slot & (c.page - 1));
+    else
+      flag_status(r.status, DFLASH_STATUS_BAD_PAGE);
+    return p;
   }
-  const int slot = q.C + j, col = slot >> c.page_log2;
-  const int pg = col < c.cols ? c.table[static_cast<int64_t>(s) * c.cols + col] : -1;
-  if (pg >= 0 && pg < c.n_pages)
-    p.row = static_cast<int64_t>(pg) * c.nkv * c.page + (slot & (c.page - 1));
-  else
-    flag_status(r.status, DFLASH_STATUS_BAD_PAGE);
   return p;
 }
 
-struct Bf16x16 {
-  uint4 a, b;
-};
-__device__ __forceinline__ Bf16x16 load16(const __nv_bfloat16* p) {
-  const uint4* q = reinterpret_cast<const uint4*>(p);
-  return Bf16x16{q[0], q[1]};
-}
-__device__ __forceinline__ void unpack16(const Bf16x16& x, float (&v)[16]) {
-  const uint32_t w[8] = {x.a.x, x.a.y, x.a.z, x.a.w, x.b.x, x.b.y, x.b.z, x.b.w};
+__device__ __forceinline__ void unpack8(const uint4& x, float (&v)[8]) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     v[2 * i] = __uint_as_float(w[i] << 16);
     v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
-__device__ __forceinline__ Bf16x16 pack16(const float (&v)[16]) {
-  uint32_t w[8];
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
     w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  return Bf16x16{make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7])};
-}
-__device__ __forceinline__ void store16(__nv_bfloat16* p, const Bf16x16& x) {
-  uint4* q = reinterpret_cast<uint4*>(p);
-  q[0] = x.a;
-  q[1] = x.b;
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A group of 16 bf16 values to its e4m3 scale and 16 codes (low nibble first).
-__device__ __forceinline__ uint2 quantise16(const Bf16x16& x, uint8_t* scale) {
-  float v[16];
-  unpack16(x, v);
+// Half a group of 16 bf16 values (the other half is the neighbouring lane's)
+// to its 8 codes (low nibble first) and the group's e4m3 scale.
+__device__ __forceinline__ uint32_t quantise8(const uint4& x, uint8_t* scale) {
+  float v[8];
+  unpack8(x, v);
   float top = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(v[i]));
+  for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
   const float want = fminf(__fdiv_rn(top, 6.f), 448.f);
   uint16_t s2;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s2) : "f"(0.f), "f"(want));
@@ -116,43 +99,47 @@ __device__ __forceinline__ uint2 quantise16(const Bf16x16& x, uint8_t* scale) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(sh) : "h"(s2));
   const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(sh & 0xffffu)));
   *scale = static_cast<uint8_t>(s2 & 0xffu);
-  uint32_t w[2];
+  // y / s by a product with 1 / s, then to a multiple of 2^-13 (a large number
+  // added and taken away). y has 8 significant bits and s four, so y / s is
+  // either a midpoint of two codes (a multiple of 1/4) or at least 2^-7 / 15 from
+  // one, and the product is within 2^-21 of it: midpoints stay midpoints and
+  // nothing else becomes one. The sign is put back (zeros keep theirs).
+  const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+  constexpr float kGrid = 1536.f;
+  uint32_t c[4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t c[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float lo = v[8 * i + 2 * e], hi = v[8 * i + 2 * e + 1];
-      // an exact division: a value midway between two codes stays midway.
-      // A group whose scale is zero keeps its signs and no values.
-      const float qa = s > 0.f ? __fdiv_rn(lo, s) : copysignf(0.f, lo);
-      const float qb = s > 0.f ? __fdiv_rn(hi, s) : copysignf(0.f, hi);
-      asm("{\n\t.reg .b8 b;\n\t"
-          "cvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\t"
-          "mov.b32 %0, {b, 0, 0, 0};\n\t}"
-          : "=r"(c[e])
-          : "f"(qb), "f"(qa));
-    }
-    w[i] = c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24);
+  for (int e = 0; e < 4; ++e) {
+    const float qa = copysignf(__fsub_rn(__fmaf_rn(fabsf(v[2 * e]), r, kGrid), kGrid), v[2 * e]);
+    const float qb = copysignf(__fsub_rn(__fmaf_rn(fabsf(v[2 * e + 1]), r, kGrid), kGrid), v[2 * e + 1]);
+    asm("{\n\t.reg .b8 b;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\t"
+        "mov.b32 %0, {b, 0, 0, 0};\n\t}"
+        : "=r"(c[e])
+        : "f"(qb), "f"(qa));
   }
-  return make_uint2(w[0], w[1]);
+  return c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24);
 }
 
-// 16 codes and their scale to bf16.
-__device__ __forceinline__ Bf16x16 values16(uint2 codes, uint8_t scale) {
-  uint32_t sh;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(sh) : "h"(static_cast<uint16_t>(scale)));
-  const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(sh & 0xffffu)));
-  float v[16];
+// 8 codes and their scale to bf16.
+__device__ __forceinline__ uint4 values8(uint32_t codes, uint8_t scale) {
+  uint32_t sh, h[4], w[4];
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(sh) : "h"(static_cast<uint16_t>(scale * 0x101u)));
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(codes));
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t c = ((i < 8 ? codes.x : codes.y) >> (4 * (i & 7))) & 15u;
-    // e2m1 as fp32: 0, 0.5, 1, 1.5, 2, 3, 4, 6
-    const uint32_t e = (c >> 1) & 3u, m = c & 1u;
-    const float mag = e == 0u ? 0.5f * m : __uint_as_float(((e + 126u) << 23) | (m << 22));
-    v[i] = (c & 8u) ? -mag * s : mag * s;
+  for (int e = 0; e < 4; ++e) {
+    const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&h[e]), *reinterpret_cast<const __half2*>(&sh));
+    const float2 f = __half22float2(x);
+    const __nv_bfloat162 y = __floats2bfloat162_rn(f.x, f.y);
+    w[e] = *reinterpret_cast<const uint32_t*>(&y);
   }
-  return pack16(v);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 struct AppendArgs {
@@ -165,84 +152,94 @@ struct AppendArgs {
   int rope_rows, nq;
 };
 
+// 8 values of a cache row: as they are, or as codes and the group's scale.
 template <bool FP4>
-__device__ __forceinline__ void store_group(const AppendArgs& a, uint8_t* base, uint8_t* scales, int64_t row, int dim,
-                                            const Bf16x16& x) {
+__device__ __forceinline__ void store8(const AppendArgs& a, uint8_t* base, uint8_t* scales, int64_t row, int dim,
+                                       const uint4& x) {
   const int d = a.c.d;
   if (FP4) {
     uint8_t s;
-    const uint2 w = quantise16(x, &s);
-    *reinterpret_cast<uint2*>(base + row * (d / 2) + dim / 2) = w;
-    scales[row * (d / 16) + dim / 16] = s;
-  } else {
-    store16(reinterpret_cast<__nv_bfloat16*>(base) + row * d + dim, x);
+    const uint32_t w = quantise8(x, &s);
+    if (row < 0) return;
+    *reinterpret_cast<uint32_t*>(base + row * (d / 2) + dim / 2) = w;
+    if (!(dim & 8)) scales[row * (d / 16) + dim / 16] = s;
+  } else if (row >= 0) {
+    *reinterpret_cast<uint4*>(base + (row * d + dim) * 2) = x;
   }
 }
 
 template <bool FP4>
-__global__ void __launch_bounds__(kAppendThreads) page_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 8) page_append_kernel(const AppendArgs a) {
+  constexpr int kBatch = FP4 ? 2 : 4;  // heads a thread has in flight, at 64 registers
   pdl_wait();
   pdl_trigger();
   const int t = blockIdx.x;
-  const int d = a.c.d, half = d / 2, parts = d / 32;
-  const int units = (a.nq + 2 * a.c.nkv) * parts;
+  const int d = a.c.d, half = d / 2, parts = d / 16, lanes = kThreads / parts;
+  const int part = static_cast<int>(threadIdx.x) % parts, lane_h = static_cast<int>(threadIdx.x) / parts;
+  const int d0 = part * 8, d1 = half + d0;
+  const int heads = a.nq + 2 * a.c.nkv;  // queries, then K, then V
   Place place{};
-  bool placed = false;
-  for (int u0 = 0; u0 < units; u0 += kAppendThreads) {
-    const int u = u0 + static_cast<int>(threadIdx.x);
-    const int part = u % parts;
-    int hd = u / parts;
-    // queries, then K heads, then V heads
-    const int kind = hd < a.nq ? 0 : hd < a.nq + a.c.nkv ? 1 : 2;
-    hd -= kind == 0 ? 0 : kind == 1 ? a.nq : a.nq + a.c.nkv;
-    const int d0 = kind == 2 ? part * 32 : part * 16, d1 = kind == 2 ? d0 + 16 : half + d0;
-    const bool on = u < units;
-    Bf16x16 x0{}, x1{};
-    if (on) {
-      const __nv_bfloat16* src = (kind == 0   ? a.q + static_cast<int64_t>(t) * a.q_ld
-                                  : kind == 1 ? a.k + static_cast<int64_t>(t) * a.k_ld
-                                              : a.v + static_cast<int64_t>(t) * a.v_ld) +
-                                 static_cast<int64_t>(hd) * d;
-      x0 = load16(src + d0);
-      x1 = load16(src + d1);
+  float4 cs[4];  // (cos, sin) of the thread's 8 pairs, two a piece
+  for (int h0 = 0; h0 < heads; h0 += kBatch * lanes) {
+    uint4 x0[kBatch], x1[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int u = h0 + i * lanes + lane_h;
+      if (u >= heads) continue;
+      const __nv_bfloat16* src =
+          u < a.nq ? a.q + static_cast<int64_t>(t) * a.q_ld + static_cast<int64_t>(u) * d
+          : u < a.nq + a.c.nkv
+              ? a.k + static_cast<int64_t>(t) * a.k_ld + static_cast<int64_t>(u - a.nq) * d
+              : a.v + static_cast<int64_t>(t) * a.v_ld + static_cast<int64_t>(u - a.nq - a.c.nkv) * d;
+      x0[i] = *reinterpret_cast<const uint4*>(src + d0);
+      x1[i] = *reinterpret_cast<const uint4*>(src + d1);
     }
-    if (!placed) {
+    if (h0 == 0) {
       place = find_place(a.c, a.r, t);
-      placed = true;
       if (place.pos >= 0 && a.rope && place.pos >= a.rope_rows) {
         flag_status(a.r.status, DFLASH_STATUS_BAD_ROWS);
         place.pos = -1;
       }
       if (place.pos < 0) return;  // the whole CTA: one row
-    }
-    if (!on) continue;
-    if (kind != 2 && a.rope) {
-      const float4* cs = reinterpret_cast<const float4*>(a.rope + static_cast<int64_t>(place.pos) * half + d0);
-      float lo[16], hi[16];
-      unpack16(x0, lo);
-      unpack16(x1, hi);
+      if (a.rope) {
+        const float4* p = reinterpret_cast<const float4*>(a.rope + static_cast<int64_t>(place.pos) * half + d0);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 w = cs[i];  // (cos, sin) of two dims
-        const float a0 = lo[2 * i], b0 = hi[2 * i], a1 = lo[2 * i + 1], b1 = hi[2 * i + 1];
-        lo[2 * i] = __fsub_rn(__fmul_rn(a0, w.x), __fmul_rn(b0, w.y));
-        hi[2 * i] = __fadd_rn(__fmul_rn(b0, w.x), __fmul_rn(a0, w.y));
-        lo[2 * i + 1] = __fsub_rn(__fmul_rn(a1, w.z), __fmul_rn(b1, w.w));
-        hi[2 * i + 1] = __fadd_rn(__fmul_rn(b1, w.z), __fmul_rn(a1, w.w));
+        for (int i = 0; i < 4; ++i) cs[i] = p[i];
       }
-      x0 = pack16(lo);
-      x1 = pack16(hi);
     }
-    if (kind == 0) {
-      __nv_bfloat16* dst = a.q_out + static_cast<int64_t>(t) * a.q_out_ld + static_cast<int64_t>(hd) * d;
-      store16(dst + d0, x0);
-      store16(dst + d1, x1);
-    } else if (place.row >= 0) {
-      const int64_t row = place.row + static_cast<int64_t>(hd) * a.c.page;
-      uint8_t* base = kind == 1 ? a.c.k : a.c.v;
-      uint8_t* scales = kind == 1 ? a.c.ks : a.c.vs;
-      store_group<FP4>(a, base, scales, row, d0, x0);
-      store_group<FP4>(a, base, scales, row, d1, x1);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int u = h0 + i * lanes + lane_h;
+      const bool on = u < heads;
+      if (a.rope && u < a.nq + a.c.nkv) {
+        float lo[8], hi[8];
+        unpack8(x0[i], lo);
+        unpack8(x1[i], hi);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float4 w = cs[e];
+          const float a0 = lo[2 * e], b0 = hi[2 * e], a1 = lo[2 * e + 1], b1 = hi[2 * e + 1];
+          lo[2 * e] = __fsub_rn(__fmul_rn(a0, w.x), __fmul_rn(b0, w.y));
+          hi[2 * e] = __fadd_rn(__fmul_rn(b0, w.x), __fmul_rn(a0, w.y));
+          lo[2 * e + 1] = __fsub_rn(__fmul_rn(a1, w.z), __fmul_rn(b1, w.w));
+          hi[2 * e + 1] = __fadd_rn(__fmul_rn(b1, w.z), __fmul_rn(a1, w.w));
+        }
+        x0[i] = pack8(lo);
+        x1[i] = pack8(hi);
+      }
+      if (on && u < a.nq) {
+        __nv_bfloat16* dst = a.q_out + static_cast<int64_t>(t) * a.q_out_ld + static_cast<int64_t>(u) * d;
+        *reinterpret_cast<uint4*>(dst + d0) = x0[i];
+        *reinterpret_cast<uint4*>(dst + d1) = x1[i];
+      }
+      // quantising shuffles: every lane of a warp that holds a K or V head takes part
+      if (__any_sync(0xffffffffu, on && u >= a.nq)) {
+        const bool is_k = u < a.nq + a.c.nkv;
+        const int hd = u - a.nq - (is_k ? 0 : a.c.nkv);
+        const int64_t row = on && u >= a.nq && place.row >= 0 ? place.row + static_cast<int64_t>(hd) * a.c.page : -1;
+        store8<FP4>(a, is_k ? a.c.k : a.c.v, is_k ? a.c.ks : a.c.vs, row, d0, x0[i]);
+        store8<FP4>(a, is_k ? a.c.k : a.c.v, is_k ? a.c.ks : a.c.vs, row, d1, x1[i]);
+      }
     }
   }
 }
@@ -255,28 +252,42 @@ struct ReadArgs {
 };
 
 template <bool FP4>
-__global__ void __launch_bounds__(kAppendThreads) page_read_kernel(const ReadArgs a) {
+__global__ void __launch_bounds__(kThreads) page_read_kernel(const ReadArgs a) {
+  constexpr int kBatch = 4;  // pieces a lane has in flight
   pdl_wait();
   pdl_trigger();
-  const int t = blockIdx.x;
+  const int t = blockIdx.x * (kThreads / 32) + (static_cast<int>(threadIdx.x) >> 5);  // a warp a row
+  if (t >= a.r.T) return;
   const Place place = find_place(a.c, a.r, t);
   if (place.pos < 0 || place.row < 0) return;
-  const int d = a.c.d, groups = d / 16;
-  const int units = 2 * a.c.nkv * groups;
-  for (int u = threadIdx.x; u < units; u += kAppendThreads) {
-    const int grp = u % groups, kv = (u / groups) / a.c.nkv, hd = (u / groups) % a.c.nkv;
-    const int64_t row = place.row + static_cast<int64_t>(hd) * a.c.page;
-    const uint8_t* base = kv ? a.c.v : a.c.k;
-    Bf16x16 x;
-    if (FP4) {
-      const uint8_t* sc = kv ? a.c.vs : a.c.ks;
-      x = values16(*reinterpret_cast<const uint2*>(base + row * (d / 2) + grp * 8), sc[row * groups + grp]);
-    } else {
-      x = load16(reinterpret_cast<const __nv_bfloat16*>(base) + row * d + grp * 16);
+  const int d = a.c.d, pieces = d / 8, log2p = d == 128 ? 4 : d == 64 ? 3 : 2;
+  const int units = 2 * a.c.nkv * pieces;
+  for (int u0 = threadIdx.x & 31; u0 < units; u0 += 32 * kBatch) {
+    uint4 x[kBatch];
+    uint8_t sc[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int u = u0 + 32 * i, d0 = (u & (pieces - 1)) * 8, head = u >> log2p;
+      if (u >= units) continue;
+      const bool kv = head >= a.c.nkv;
+      const int64_t row = place.row + static_cast<int64_t>(kv ? head - a.c.nkv : head) * a.c.page;
+      const uint8_t* base = kv ? a.c.v : a.c.k;
+      if (FP4) {
+        x[i].x = *reinterpret_cast<const uint32_t*>(base + row * (d / 2) + d0 / 2);
+        sc[i] = (kv ? a.c.vs : a.c.ks)[row * (d / 16) + d0 / 16];
+      } else {
+        x[i] = *reinterpret_cast<const uint4*>(base + (row * d + d0) * 2);
+      }
     }
-    __nv_bfloat16* dst = (kv ? a.v + static_cast<int64_t>(t) * a.v_ld : a.k + static_cast<int64_t>(t) * a.k_ld) +
-                         static_cast<int64_t>(hd) * d + grp * 16;
-    store16(dst, x);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int u = u0 + 32 * i, d0 = (u & (pieces - 1)) * 8, head = u >> log2p;
+      if (u >= units) continue;
+      const bool kv = head >= a.c.nkv;
+      __nv_bfloat16* dst = kv ? a.v + static_cast<int64_t>(t) * a.v_ld + static_cast<int64_t>(head - a.c.nkv) * d
+                              : a.k + static_cast<int64_t>(t) * a.k_ld + static_cast<int64_t>(head) * d;
+      *reinterpret_cast<uint4*>(dst + d0) = FP4 ? values8(x[i].x, sc[i]) : x[i];
+    }
   }
 }
 
@@ -290,7 +301,7 @@ int launch_page_append(const PagesArgs& c, const RowsArgs& r, const __nv_bfloat1
                      2.0 * c.nkv * (fp4 ? c.d / 2 + c.d / 16 : 2 * c.d) + (rope ? 4.0 * c.d : 0.0);
   TraceScope ts(st, "page_append", row * r.T, 0.0);
   const cudaError_t e = launch_pdl(fp4 ? page_append_kernel<true> : page_append_kernel<false>, dim3(r.T),
-                                   dim3(kAppendThreads), 0, st, a);
+                                   dim3(kThreads), 0, st, a);
   count_launch();
   return cuda_status(e);
 }
@@ -299,8 +310,8 @@ int launch_page_read(const PagesArgs& c, const RowsArgs& r, __nv_bfloat16* k, in
                      int64_t v_ld, bool fp4, cudaStream_t st) {
   ReadArgs a{c, r, k, v, k_ld, v_ld};
   TraceScope ts(st, "page_read", 2.0 * c.nkv * r.T * (2.0 * c.d + (fp4 ? c.d / 2 + c.d / 16 : 2 * c.d)), 0.0);
-  const cudaError_t e = launch_pdl(fp4 ? page_read_kernel<true> : page_read_kernel<false>, dim3(r.T),
-                                   dim3(kAppendThreads), 0, st, a);
+  const cudaError_t e = launch_pdl(fp4 ? page_read_kernel<true> : page_read_kernel<false>,
+                                   dim3((r.T + kThreads / 32 - 1) / (kThreads / 32)), dim3(kThreads), 0, st, a);
   count_launch();
   return cuda_status(e);
 }
