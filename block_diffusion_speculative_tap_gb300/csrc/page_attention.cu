@@ -164,8 +164,7 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int64_t f = static_cast<int64_t>(sg.tile) * kTile + 8 * b + 2 * t + i;
-      const int j = static_cast<int>(f / a.G);
+      const int j = static_cast<int>(static_cast<unsigned>(sg.tile * kTile + 8 * b + 2 * t + i) / a.G);
       RowView& v = rv[b][i];
       v.j = j < q.n ? j : -1;
       v.pos = v.j >= 0 ? row_pos(a.r, q, j) : 0;
@@ -182,14 +181,13 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
   const int hi = q.C + (a.mode == DFLASH_MASK_CAUSAL ? j_max + 1 : q.n);
   lo = min(lo, q.C);
   const int sinks = min(a.sinks, hi);
-  const UnitRange ur = unit_range(lo, hi, a.sinks, kKeys);
-  const int i0 = static_cast<int>(static_cast<long long>(ur.n) * sg.x0 / sg.u);
-  const int i1 = static_cast<int>(static_cast<long long>(ur.n) * sg.x1 / sg.u);
+  const UnitRange ur = unit_range(lo, hi, a.sinks, a.unit_log2);
+  const int i0 = static_cast<int>(div_up_to_64(static_cast<long long>(ur.n) * sg.x0, sg.u));
+  const int i1 = static_cast<int>(div_up_to_64(static_cast<long long>(ur.n) * sg.x1, sg.u));
 
   const int* table = a.c.table + static_cast<int64_t>(sg.s) * a.c.cols;
   auto unit_at = [&](int i) { return i < ur.nsink ? i : ur.first + (i - ur.nsink); };
-  int pg[kSub];
-  auto fetch_pages = [&](int i) {
+  auto fetch_pages = [&](int i, int (&pg)[kSub]) {
 #pragma unroll
     for (int b = 0; b < kSub; ++b) {
       pg[b] = -1;
@@ -206,7 +204,7 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
   uint8_t* ring = smem + warp * kST * G_::kStage;
   const uint32_t ring_u = smem_u32(ring);
   uint32_t pres = 0;  // of the units in flight, newest in the low bits: which 16-slot pieces are there
-  auto issue = [&](int i, int stage) {
+  auto issue = [&](int i, int stage, const int (&pg)[kSub]) {
     pres <<= kSub;
     if (i < i1) {
       const int kb = unit_at(i) * kKeys;
@@ -240,22 +238,21 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
     cp_commit();
   };
 
-  // the stages ahead of the first unit; pages of the next one are looked up
-  // while a unit's copies are issued
-  fetch_pages(i0 + warp);
+  // the stages ahead of the first unit; all their pages are looked up at once,
+  // and later ones while a unit's copies are issued
+  int pg[kST][kSub];
 #pragma unroll
-  for (int s = 0; s < kST - 1; ++s) {
-    issue(i0 + warp + s * kWarps, s);
-    fetch_pages(i0 + warp + (s + 1) * kWarps);
-  }
+  for (int s = 0; s < kST; ++s) fetch_pages(i0 + warp + s * kWarps, pg[s]);
+#pragma unroll
+  for (int s = 0; s < kST - 1; ++s) issue(i0 + warp + s * kWarps, s, pg[s]);
 
   // queries as B fragments (row g of a block of 8), in the order of dims that K's pieces give
   uint32_t qb[NB][D / 16][2];
   float sc[NB][2];
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
-    const int64_t f = static_cast<int64_t>(sg.tile) * kTile + 8 * b + g;
-    const int j = static_cast<int>(f / a.G), hd = static_cast<int>(f - static_cast<int64_t>(j) * a.G);
+    const unsigned f = static_cast<unsigned>(sg.tile * kTile + 8 * b + g);
+    const int j = static_cast<int>(f / a.G), hd = static_cast<int>(f - j * a.G);
     const __nv_bfloat16* qp =
         j < q.n ? a.q + static_cast<int64_t>(q.row0 + j) * a.q_ld + (h * a.G + hd) * D : nullptr;
     constexpr int kPieces = D / 32;  // 16-byte pieces of a row a lane holds
@@ -317,8 +314,8 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
   for (int i = i0 + warp; i < i1; i += kWarps) {
     {
       const int ns = stage == 0 ? kST - 1 : stage - 1;
-      issue(i + (kST - 1) * kWarps, ns);
-      fetch_pages(i + kST * kWarps);
+      issue(i + (kST - 1) * kWarps, ns, pg[kST - 1]);
+      fetch_pages(i + kST * kWarps, pg[kST - 1]);
     }
     cp_wait<kST - 1>();
     __syncwarp();
@@ -580,7 +577,7 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
   __syncthreads();
   for (int x = threadIdx.x; x < kTile * (D / 4); x += kWarps * 32) {
     const int r = x / (D / 4), d4 = (x % (D / 4)) * 4;
-    const int64_t f = static_cast<int64_t>(sg.tile) * kTile + r;
+    const unsigned f = static_cast<unsigned>(sg.tile * kTile + r);
     const int j = static_cast<int>(f / a.G);
     if (j >= q.n) continue;
     float M = -INFINITY;
@@ -604,7 +601,7 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
       *reinterpret_cast<float4*>(a.part_o + (part_row + r) * D + d4) = acc;
       if (d4 == 0) *reinterpret_cast<float2*>(a.part_ml + (part_row + r) * 2) = make_float2(M, den);
     } else {
-      const int hd = static_cast<int>(f - static_cast<int64_t>(j) * a.G);
+      const int hd = static_cast<int>(f - j * a.G);
       const float inv = M == -INFINITY ? 0.f : 1.f / den;
       uint2 w;
       w.x = pack2(acc.x * inv, acc.y * inv, false);
@@ -619,7 +616,11 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
 // Joins the parts of the tiles that a boundary between two CTAs' shares cuts:
 // a CTA a boundary and rows of its tile, a warp a row.
 constexpr int kCombineRows = 8;
-template <int D>
+// kAhead: parts whose rows are loaded before any is used. A token of 8 kv heads
+// over all SMs is 19 parts of few rows (20 ahead: 15.4 -> 12.8 us a call); the
+// large tiles have two or three parts of many rows, where the registers would
+// cost residence (blocks 77 -> 103 us with 20).
+template <int D, int kAhead>
 __global__ void __launch_bounds__(kCombineRows * 32) page_combine_kernel(const __grid_constant__ PageAttnArgs a) {
   constexpr int kE = D / 32;
   __shared__ Segment seg_s;
@@ -637,8 +638,9 @@ __global__ void __launch_bounds__(kCombineRows * 32) page_combine_kernel(const _
       const long long from = at - sg.x0, to = from + sg.u, before = sh.start(a, b - 1);
       if (sg.x0 > 0 && before <= from) {  // the first boundary inside the tile
         slot = static_cast<int>(2 * (b - 1) + (before == from ? 0 : 1));
-        parts = 2;
-        while (b + parts - 1 < sh.ctas && sh.start(a, b + parts - 1) < to) ++parts;
+        // the CTAs whose share starts before the tile's end: start(k) < to as long as k < to * ctas / total
+        const long long total = sh.line * a.c.nkv;
+        parts = static_cast<int>(div_up_to_64(to * sh.ctas + total - 1, total) - (b - 1));
       }
     }
     if (lane == 0) {
@@ -656,35 +658,57 @@ __global__ void __launch_bounds__(kCombineRows * 32) page_combine_kernel(const _
   const int r = blockIdx.y * kCombineRows + warp;
   bool bad;
   const StreamRows q = stream_rows(a.r, sg.s, &bad);
-  const int64_t f = static_cast<int64_t>(sg.tile) * a.tile + r;
+  const unsigned f = static_cast<unsigned>(sg.tile * a.tile + r);
   const int j = static_cast<int>(f / a.G);
   if (r >= a.tile || j >= q.n) return;
   const int next = 2 * (static_cast<int>(blockIdx.x) + 1);  // slot of the second part; the others follow by 2
   auto row_of = [&](int k) { return static_cast<int64_t>(k == 0 ? slot_s : next + 2 * (k - 1)) * a.tile + r; };
-  float M = -INFINITY;
-  for (int k = lane; k < parts; k += 32) M = fmaxf(M, a.part_ml[row_of(k) * 2]);
-#pragma unroll
-  for (int x = 16; x >= 1; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+  float M = -INFINITY, den = 0.f;
   float acc[kE] = {};
-  float den = 0.f;
-  if (M != -INFINITY) {
-#pragma unroll 8
-    for (int k = 0; k < parts; ++k) {
-      const int64_t row = row_of(k);
-      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + row * 2);
-      const float w = ex2f(ml.x - M);
-      den = fmaf(w, ml.y, den);
-      const float* src = a.part_o + row * D + lane * kE;
-      float v[kE];
+  // 32 parts at a time: a lane a part's (maximum, sum), all parts' rows in flight
+  for (int k0 = 0; k0 < parts; k0 += 32) {
+    const int n = min(32, parts - k0);
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < n) ml = *reinterpret_cast<const float2*>(a.part_ml + row_of(k0 + lane) * 2);
+    float mx = ml.x;
+    auto load = [&](int k, float (&v)[kE]) {
+      const float* src = a.part_o + row_of(k0 + k) * D + lane * kE;
       if (kE == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
       else if (kE == 2) *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
       else v[0] = *src;
+    };
+    float v[kAhead][kE];
 #pragma unroll
-      for (int e = 0; e < kE; ++e) acc[e] = fmaf(w, v[e], acc[e]);
+    for (int k = 0; k < kAhead; ++k)
+      if (k < n) load(k, v[k]);
+#pragma unroll
+    for (int x = 16; x >= 1; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+    const float top = fmaxf(M, mx);
+    if (top == -INFINITY) continue;
+    const float old = ex2f(M - top), w = ex2f(ml.x - top);
+    float d32 = w * ml.y;
+#pragma unroll
+    for (int x = 16; x >= 1; x >>= 1) d32 += __shfl_xor_sync(0xffffffffu, d32, x);
+    den = fmaf(den, old, d32);
+#pragma unroll
+    for (int e = 0; e < kE; ++e) acc[e] *= old;
+    M = top;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (k < n) {
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+#pragma unroll
+        for (int e = 0; e < kE; ++e) acc[e] = fmaf(wk, v[k][e], acc[e]);
+      }
+    for (int k = kAhead; k < n; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      load(k, v[0]);
+#pragma unroll
+      for (int e = 0; e < kE; ++e) acc[e] = fmaf(wk, v[0][e], acc[e]);
     }
   }
   const float inv = M == -INFINITY ? 0.f : 1.f / den;
-  const int hd = static_cast<int>(f - static_cast<int64_t>(j) * a.G);
+  const int hd = static_cast<int>(f - j * a.G);
   __nv_bfloat16* dst = a.out + static_cast<int64_t>(q.row0 + j) * a.out_ld + (sg.h * a.G + hd) * D + lane * kE;
   if (kE == 4) {
     uint2 w;
@@ -723,7 +747,7 @@ int launch_small_any(const PageAttnArgs& a, const PagePlan& p, bool fp4, cudaStr
 
 template <int D>
 int launch_combine(const PageAttnArgs& a, const PagePlan& p, cudaStream_t st) {
-  const cudaError_t e = launch_pdl(page_combine_kernel<D>,
+  const cudaError_t e = launch_pdl(a.tile > 16 ? page_combine_kernel<D, 3> : page_combine_kernel<D, 20>,
                                    dim3(static_cast<unsigned>(p.target - 1),
                                         static_cast<unsigned>((a.tile + kCombineRows - 1) / kCombineRows)),
                                    dim3(kCombineRows * 32), 0, st, a);

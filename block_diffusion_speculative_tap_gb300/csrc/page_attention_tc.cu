@@ -234,9 +234,9 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
   const StreamRows q = stream_rows(a.r, it.s, &bad);
   // what the tile's rows see: from the window of the lowest position to the
   // end of the last row's (positions of a tree are looked up)
-  const int64_t f0 = static_cast<int64_t>(it.tile) * a.tile;
+  const unsigned f0 = static_cast<unsigned>(it.tile * a.tile);
   const int j_lo = static_cast<int>(f0 / a.G);
-  const int j_hi = min(q.n - 1, static_cast<int>((f0 + a.tile - 1) / a.G));
+  const int j_hi = min(q.n - 1, static_cast<int>((f0 + a.tile - 1u) / a.G));
   int pos_lo = q.C + j_lo, pos_hi = q.C + j_hi;
   if (a.r.depth && a.window > 0) {
     pos_lo = 0x7fffffff;
@@ -256,9 +256,9 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
   const bool plain = a.mode != DFLASH_MASK_TREE && a.r.depth == nullptr;  // visibility is a range of slots
   // slots below this are seen by every row as far as the rows' order goes
   const int all_end = !plain ? q.C : a.mode == DFLASH_MASK_CAUSAL ? q.C + j_lo + 1 : q.C + q.n;
-  const UnitRange ur = unit_range(lo, hi, a.sinks, kTK);
-  const int i0 = static_cast<int>(static_cast<long long>(ur.n) * it.x0 / it.u);
-  const int i1 = static_cast<int>(static_cast<long long>(ur.n) * it.x1 / it.u);
+  const UnitRange ur = unit_range(lo, hi, a.sinks, a.unit_log2);
+  const int i0 = static_cast<int>(div_up_to_64(static_cast<long long>(ur.n) * it.x0, it.u));
+  const int i1 = static_cast<int>(div_up_to_64(static_cast<long long>(ur.n) * it.x1, it.u));
   const int nt = i1 - i0;  // key tiles
   auto slot0 = [&](int t) {
     const int i = i0 + t;
@@ -521,10 +521,10 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
     const int r = q4 * 32 + lane;
     const uint32_t tl = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
     const uint32_t ts = tl + s * 128, to = tl + Ge::kColO + s * D;
-    const int64_t f = f0 + (PAIR ? s * kMRows : 0) + r;
+    const unsigned f = f0 + (PAIR ? s * kMRows : 0) + r;
     RowView rv;
     const int jr = static_cast<int>(f / a.G);
-    const int hd = static_cast<int>(f - static_cast<int64_t>(jr) * a.G);
+    const int hd = static_cast<int>(f - jr * a.G);
     rv.j = jr < q.n ? jr : -1;
     rv.pos = rv.j >= 0 ? row_pos(a.r, q, jr) : 0;
     rv.back = a.window > 0 ? max(0, rv.pos - a.window + 1) : 0;

@@ -38,8 +38,8 @@ struct PageAttnArgs {
   int nq, G;
   float scale;           // softmax scale times log2(e)
   // work split (see Share)
-  int unit;              // slots a unit of the split
-  int tile;              // rows (query row x head of the group) a tile
+  int unit_log2;         // slots a unit of the split
+  int tile, tile_log2;   // rows (query row x head of the group) a tile
   int target;            // CTAs of one wave
   int min_units;         // fewest units a CTA's share has
   int no_split;          // tiles of up to this many units are not split
@@ -71,11 +71,12 @@ __device__ __forceinline__ StreamRows stream_rows(const RowsArgs& r, int s, bool
 struct UnitRange {
   int nsink, first, n;
 };
-__device__ __forceinline__ UnitRange unit_range(int lo, int hi, int sinks, int unit) {
+__device__ __forceinline__ UnitRange unit_range(int lo, int hi, int sinks, int unit_log2) {
   UnitRange u;
-  const int end = (hi + unit - 1) / unit;
-  u.first = min(lo / unit, end);
-  u.nsink = lo > 0 ? min((min(sinks, hi) + unit - 1) / unit, u.first) : 0;
+  const int more = (1 << unit_log2) - 1;
+  const int end = (hi + more) >> unit_log2;
+  u.first = min(lo >> unit_log2, end);
+  u.nsink = lo > 0 ? min((min(sinks, hi) + more) >> unit_log2, u.first) : 0;
   u.n = u.nsink + end - u.first;
   return u;
 }
@@ -89,13 +90,17 @@ __device__ __forceinline__ UnitRange unit_range(int lo, int hi, int sinks, int u
 // a CTA's first segment and 2b + 1 for its last, and page_combine_kernel joins
 // the parts. With many tiles, or short ones, every CTA takes whole tiles
 // instead.
+__device__ __forceinline__ long long div_up_to_64(long long a, long long b) {  // a >= 0, b > 0; mostly 32 bits
+  if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+  return a / b;
+}
 struct Share {
   long long line;   // units of a kv head
   long long tiles;  // tiles of a kv head
   long long ctas;   // B
   bool whole;       // a tile a CTA
   __device__ __forceinline__ long long start(const PageAttnArgs& a, long long b) const {
-    return whole ? b : line * a.c.nkv * b / ctas;
+    return whole ? b : div_up_to_64(line * a.c.nkv * b, ctas);
   }
 };
 struct Segment {
@@ -107,10 +112,10 @@ __device__ __forceinline__ int stream_units(const PageAttnArgs& a, int s, int* m
   bool bad;
   const StreamRows q = stream_rows(a.r, s, &bad);
   if (bad && flag) flag_status(a.r.status, DFLASH_STATUS_BAD_ROWS);
-  *mt = static_cast<int>((static_cast<int64_t>(q.n) * a.G + a.tile - 1) / a.tile);
+  *mt = (q.n * a.G + (1 << a.tile_log2) - 1) >> a.tile_log2;  // max_rows * G is under 2^31
   if (q.n == 0) return 0;
   const int lo = a.window > 0 ? max(0, q.C - a.window + 1) : 0;
-  return unit_range(lo, q.C + q.n, a.sinks, a.unit).n;
+  return unit_range(lo, q.C + q.n, a.sinks, a.unit_log2).n;
 }
 
 // One warp; every lane gets the answer.
@@ -138,7 +143,7 @@ __device__ __forceinline__ Share share_of(const PageAttnArgs& a) {
   if (sh.whole) {
     sh.ctas = tiles * a.c.nkv;
   } else {
-    const long long b = (line * a.c.nkv + a.min_units - 1) / a.min_units;
+    const long long b = div_up_to_64(line * a.c.nkv + a.min_units - 1, a.min_units);
     sh.ctas = b < a.target ? b : a.target;
   }
   return sh;
@@ -150,7 +155,7 @@ __device__ __forceinline__ Segment segment_at(const PageAttnArgs& a, const Share
   const int lane = threadIdx.x & 31;
   const long long per = sh.whole ? sh.tiles : sh.line;
   Segment g;
-  g.h = static_cast<int>(at / per);
+  g.h = static_cast<int>(div_up_to_64(at, per));
   const long long r = at - g.h * per;
   long long base = 0;
   g.s = g.tile = g.u = g.x0 = g.x1 = 0;
@@ -171,7 +176,7 @@ __device__ __forceinline__ Segment segment_at(const PageAttnArgs& a, const Share
       g.s = s0 + l;
       g.u = __shfl_sync(0xffffffffu, u, l);
       const int tiles = __shfl_sync(0xffffffffu, mt, l);
-      const int tile = static_cast<int>(sh.whole ? rel : rel / g.u);
+      const int tile = static_cast<int>(sh.whole ? rel : div_up_to_64(rel, g.u));
       g.x0 = sh.whole ? 0 : static_cast<int>(rel - static_cast<long long>(tile) * g.u);
       g.x1 = g.u;
       g.tile = tiles - 1 - tile;  // the last rows see most: whole tiles start with them

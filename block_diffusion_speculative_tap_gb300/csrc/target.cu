@@ -81,12 +81,20 @@ size_t attention_ws(const PagePlan& p, const dflash_pages& c) {
   return p.split ? static_cast<size_t>(2 * p.target) * p.tile * (c.head_dim + 2) * sizeof(float) : 0;
 }
 
-int check_heads(const dflash_pages* c, int nq) {
-  return nq < 1 || nq % c->n_kv_heads || nq / c->n_kv_heads > DFLASH_MAX_PAGE_GROUP ? DFLASH_E_SHAPE : DFLASH_OK;
+int check_heads(const dflash_pages* c, const dflash_rows* r, int nq) {
+  if (nq < 1 || nq % c->n_kv_heads || nq / c->n_kv_heads > DFLASH_MAX_PAGE_GROUP) return DFLASH_E_SHAPE;
+  // a stream's (row, head of a group) pairs are counted in 31 bits, tiles of 256 of them included
+  return static_cast<int64_t>(r->max_rows) * (nq / c->n_kv_heads) > 0x7fffffff - 256 ? DFLASH_E_SHAPE : DFLASH_OK;
 }
 
 // the grid's x axis holds the call's CTAs
 int check_ctas(const PagePlan& p) { return p.ctas > 0x7fffffff ? DFLASH_E_SHAPE : DFLASH_OK; }
+
+int log2_of(int x) {
+  int n = 0;
+  while ((1 << n) < x) ++n;
+  return n;
+}
 
 }  // namespace
 
@@ -129,7 +137,7 @@ int dflash_page_read(const dflash_pages* c, const dflash_rows* r, void* k, int64
 int dflash_page_attention_workspace_bytes(const dflash_pages* c, const dflash_rows* r, int n_q_heads, size_t* bytes) {
   int rc = check_pages(c);
   if (!rc) rc = check_rows(c, r);
-  if (!rc) rc = check_heads(c, n_q_heads);
+  if (!rc) rc = check_heads(c, r, n_q_heads);
   if (rc) return rc;
   if (!bytes) return DFLASH_E_INVALID_ARG;
   *bytes = 0;
@@ -146,7 +154,7 @@ int dflash_page_attention(const dflash_pages* c, const dflash_rows* r, int n_q_h
                           dflash_stream_t stream) {
   int rc = check_pages(c);
   if (!rc) rc = check_rows(c, r);
-  if (!rc) rc = check_heads(c, n_q_heads);
+  if (!rc) rc = check_heads(c, r, n_q_heads);
   if (rc) return rc;
   if (!(scale > 0.f) || scale > 3.0e38f || window < 0 || sinks < 0) return DFLASH_E_INVALID_ARG;
   if (mask_mode != DFLASH_MASK_CAUSAL && mask_mode != DFLASH_MASK_BLOCK && mask_mode != DFLASH_MASK_TREE)
@@ -177,8 +185,9 @@ int dflash_page_attention(const dflash_pages* c, const dflash_rows* r, int n_q_h
   a.nq = n_q_heads;
   a.G = n_q_heads / c->n_kv_heads;
   a.scale = scale * 1.4426950408889634f;
-  a.unit = p.unit;
+  a.unit_log2 = log2_of(p.unit);
   a.tile = p.tile;
+  a.tile_log2 = log2_of(p.tile);
   a.target = p.target;
   a.min_units = p.min_units;
   a.no_split = p.no_split;

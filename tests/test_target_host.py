@@ -84,6 +84,7 @@ def test_pages_and_rows_are_refused_by_every_call(A):
 def test_attention_refusals(A):
     for nq in (0, -8, 12, 8 * 129):
         assert attend(A, nq=nq) == -5, nq
+    assert attend(A, r=rows(A, max_rows=1 << 29)) == -5  # 2^29 rows of four heads a kv head
     nan, inf = float("nan"), float("inf")
     for bad in (dict(scale=0.0), dict(scale=-1.0), dict(scale=nan), dict(scale=inf), dict(window=-1), dict(sinks=-1),
                 dict(mode=3), dict(mode=-1), dict(mode=2), dict(mode=2, mask=P, mask_ld=0),
