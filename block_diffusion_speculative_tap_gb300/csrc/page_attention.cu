@@ -145,45 +145,16 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   pdl_wait();
   pdl_trigger();
-  if (warp == 0) run_begin(a, &run);
   for (bool first = true;; first = false) {
-  if (warp == 0) run_next(a, &run);
+  if (warp == 0) run_next(a, &run, first);
   __syncthreads();
   if (!run.left) return;
-  const Segment sg = run.seg;
-  const int h = sg.h;
+  const Segment& sg = run.seg;
+  const StreamRows q = sg.q;
+  const int h = sg.h, lo = sg.lo, lo_max = sg.lo_max, hi = sg.hi, sinks = sg.sinks, i0 = sg.i0, i1 = sg.i1;
+  const UnitRange ur = sg.ur;
   const bool part = sg.x0 > 0 || sg.x1 < sg.u;
   const int64_t part_row = (2ll * blockIdx.x + (first ? 0 : 1)) * kTile;
-  bool bad;
-  const StreamRows q = stream_rows(a.r, sg.s, &bad);
-
-  // this lane's rows 8b + 2t, 8b + 2t + 1 of the scores, and what the tile's rows see
-  RowView rv[NB][2];
-  int lo = 0x7fffffff, lo_max = -1, j_max = 0;
-#pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int j = static_cast<int>(static_cast<unsigned>(sg.tile * kTile + 8 * b + 2 * t + i) / a.G);
-      RowView& v = rv[b][i];
-      v.j = j < q.n ? j : -1;
-      v.pos = v.j >= 0 ? row_pos(a.r, q, j) : 0;
-      v.back = a.window > 0 ? max(0, v.pos - a.window + 1) : 0;
-      if (v.j >= 0) {
-        lo = min(lo, v.back);
-        lo_max = max(lo_max, v.back);
-        j_max = max(j_max, j);
-      }
-    }
-  lo = __reduce_min_sync(0xffffffffu, lo);
-  lo_max = __reduce_max_sync(0xffffffffu, lo_max);
-  j_max = __reduce_max_sync(0xffffffffu, j_max);
-  const int hi = q.C + (a.mode == DFLASH_MASK_CAUSAL ? j_max + 1 : q.n);
-  lo = min(lo, q.C);
-  const int sinks = min(a.sinks, hi);
-  const UnitRange ur = unit_range(lo, hi, a.sinks, a.unit_log2);
-  const int i0 = static_cast<int>(div_up_to_64(static_cast<long long>(ur.n) * sg.x0, sg.u));
-  const int i1 = static_cast<int>(div_up_to_64(static_cast<long long>(ur.n) * sg.x1, sg.u));
 
   const int* table = a.c.table + static_cast<int64_t>(sg.s) * a.c.cols;
   auto unit_at = [&](int i) { return i < ur.nsink ? i : ur.first + (i - ur.nsink); };
@@ -245,6 +216,19 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
   for (int s = 0; s < kST; ++s) fetch_pages(i0 + warp + s * kWarps, pg[s]);
 #pragma unroll
   for (int s = 0; s < kST - 1; ++s) issue(i0 + warp + s * kWarps, s, pg[s]);
+
+  // this lane's rows 8b + 2t, 8b + 2t + 1 of the scores
+  RowView rv[NB][2];
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int j = static_cast<int>(static_cast<unsigned>(sg.tile * kTile + 8 * b + 2 * t + i) / a.G);
+      RowView& v = rv[b][i];
+      v.j = j < q.n ? j : -1;
+      v.pos = v.j >= 0 ? row_pos(a.r, q, j) : 0;
+      v.back = a.window > 0 ? max(0, v.pos - a.window + 1) : 0;
+    }
 
   // queries as B fragments (row g of a block of 8), in the order of dims that K's pieces give
   uint32_t qb[NB][D / 16][2];
@@ -629,18 +613,20 @@ __global__ void __launch_bounds__(kCombineRows * 32) page_combine_kernel(const _
   // row_start and lens were complete before the attention kernel let this one start
   if (warp == 0) {
     int parts = 0, slot = 0;
-    const Share sh = share_of(a);
-    const long long b = blockIdx.x + 1ll;
+    LaneStream x;
+    const Share sh = share_of(a, x);
+    const int b = static_cast<int>(blockIdx.x) + 1;
     Segment sg{};
     if (!sh.whole && b < sh.ctas) {
-      const long long at = sh.start(a, b);
-      sg = segment_at(a, sh, at);
-      const long long from = at - sg.x0, to = from + sg.u, before = sh.start(a, b - 1);
-      if (sg.x0 > 0 && before <= from) {  // the first boundary inside the tile
-        slot = static_cast<int>(2 * (b - 1) + (before == from ? 0 : 1));
-        // the CTAs whose share starts before the tile's end: start(k) < to as long as k < to * ctas / total
-        const long long total = sh.line * a.c.nkv;
-        parts = static_cast<int>(div_up_to_64(to * sh.ctas + total - 1, total) - (b - 1));
+      const int at = sh.start(b);
+      if (segment_at(a, sh, at, 1, a.r.S <= 32, x, &sg)) {
+        const int from = at - sg.x0, to = from + sg.u, before = sh.start(b - 1);
+        if (sg.x0 > 0 && before <= from) {  // the first boundary inside the tile
+          slot = 2 * (b - 1) + (before == from ? 0 : 1);
+          // the CTAs whose share starts before the tile's end: total * k / ctas < to, so k < to * ctas / total
+          const long long total = static_cast<long long>(sh.line) * a.c.nkv;
+          parts = static_cast<int>((static_cast<long long>(to) * sh.ctas + total - 1) / total) - (b - 1);
+        }
       }
     }
     if (lane == 0) {
@@ -654,10 +640,9 @@ __global__ void __launch_bounds__(kCombineRows * 32) page_combine_kernel(const _
   __syncthreads();
   const int parts = parts_s;
   if (parts == 0) return;
-  const Segment sg = seg_s;
+  const Segment& sg = seg_s;
+  const StreamRows q = sg.q;
   const int r = blockIdx.y * kCombineRows + warp;
-  bool bad;
-  const StreamRows q = stream_rows(a.r, sg.s, &bad);
   const unsigned f = static_cast<unsigned>(sg.tile * a.tile + r);
   const int j = static_cast<int>(f / a.G);
   if (r >= a.tile || j >= q.n) return;
@@ -780,7 +765,8 @@ PagePlan page_attention_plan(const dflash_pages& c, const dflash_rows& r, int nq
   const int64_t by_rows = (static_cast<int64_t>(r.rows) * G + p.tile - 1) / p.tile + c.streams;
   const int64_t tiles = std::min(c.streams * per_stream, by_rows) * c.n_kv_heads;
   const int64_t units = (static_cast<int64_t>(c.table_cols) * c.page_size + p.unit - 1) / p.unit;
-  p.split = units > p.no_split;
+  // (places on the line of all units are 31 bits wide)
+  p.split = units > p.no_split && c.streams * per_stream * c.n_kv_heads < 0x7fffffff / units;
   p.ctas = std::max<int64_t>(tiles, p.split ? p.target : 0);
   return p;
 }

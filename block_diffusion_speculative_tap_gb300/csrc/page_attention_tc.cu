@@ -193,19 +193,14 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
 
   pdl_wait();
   pdl_trigger();
-  if (warp == 0) run_begin(a, run);
-  __syncthreads();
-  const bool any_work = run->at < run->end;
-  __syncthreads();  // every warp has read it before the run moves on
-  if (!any_work) return;
-  if (warp == 8) {
-    tmem_alloc(tmem_slot, 512);
-    tmem_relinquish();
-  }
   for (bool first = true;; first = false) {
   // between segments everything asynchronous has completed: the barriers start
   // again at phase 0
-  if (warp == 0) run_next(a, run);
+  if (warp == 0) run_next(a, run, first);
+  if (first && warp == 8) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
   if (threadIdx.x == 32) {
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&full[s], FP4 ? 32 * Ge::kProd : 1);
@@ -225,41 +220,17 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
   tc_fence_after();
   if (!run->left) break;
   const uint32_t tmem = *tmem_slot;
-  const Segment it = run->seg;
-  const int h = it.h;
+  const Segment& it = run->seg;
+  const StreamRows q = it.q;
+  const int h = it.h, lo = it.lo, lo_max = it.lo_max, hi = it.hi, sinks = it.sinks, i0 = it.i0;
+  const int nt = it.i1 - it.i0;  // key tiles
+  const UnitRange ur = it.ur;
   const bool split = it.x0 > 0 || it.x1 < it.u;
   const int64_t part_row = (2ll * blockIdx.x + (first ? 0 : 1)) * a.tile;
-
-  bool bad;
-  const StreamRows q = stream_rows(a.r, it.s, &bad);
-  // what the tile's rows see: from the window of the lowest position to the
-  // end of the last row's (positions of a tree are looked up)
   const unsigned f0 = static_cast<unsigned>(it.tile * a.tile);
-  const int j_lo = static_cast<int>(f0 / a.G);
-  const int j_hi = min(q.n - 1, static_cast<int>((f0 + a.tile - 1u) / a.G));
-  int pos_lo = q.C + j_lo, pos_hi = q.C + j_hi;
-  if (a.r.depth && a.window > 0) {
-    pos_lo = 0x7fffffff;
-    pos_hi = 0;
-    for (int j = j_lo + lane; j <= j_hi; j += 32) {
-      const int p = row_pos(a.r, q, j);
-      pos_lo = min(pos_lo, p);
-      pos_hi = max(pos_hi, p);
-    }
-    pos_lo = __reduce_min_sync(0xffffffffu, pos_lo);
-    pos_hi = __reduce_max_sync(0xffffffffu, pos_hi);
-  }
-  const int hi = q.C + (a.mode == DFLASH_MASK_CAUSAL ? j_hi + 1 : q.n);
-  const int lo = a.window > 0 ? min(q.C, max(0, pos_lo - a.window + 1)) : 0;
-  const int lo_max = a.window > 0 ? max(0, pos_hi - a.window + 1) : 0;
-  const int sinks = min(a.sinks, hi);
   const bool plain = a.mode != DFLASH_MASK_TREE && a.r.depth == nullptr;  // visibility is a range of slots
   // slots below this are seen by every row as far as the rows' order goes
-  const int all_end = !plain ? q.C : a.mode == DFLASH_MASK_CAUSAL ? q.C + j_lo + 1 : q.C + q.n;
-  const UnitRange ur = unit_range(lo, hi, a.sinks, a.unit_log2);
-  const int i0 = static_cast<int>(div_up_to_64(static_cast<long long>(ur.n) * it.x0, it.u));
-  const int i1 = static_cast<int>(div_up_to_64(static_cast<long long>(ur.n) * it.x1, it.u));
-  const int nt = i1 - i0;  // key tiles
+  const int all_end = !plain ? q.C : a.mode == DFLASH_MASK_CAUSAL ? q.C + it.j_lo + 1 : q.C + q.n;
   auto slot0 = [&](int t) {
     const int i = i0 + t;
     return (i < ur.nsink ? i : ur.first + (i - ur.nsink)) * kTK;

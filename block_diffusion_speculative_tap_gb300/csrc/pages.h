@@ -89,136 +89,189 @@ __device__ __forceinline__ UnitRange unit_range(int lo, int hi, int sinks, int u
 // segments, each (part of) one tile; a part goes to the workspace, slot 2b for
 // a CTA's first segment and 2b + 1 for its last, and page_combine_kernel joins
 // the parts. With many tiles, or short ones, every CTA takes whole tiles
-// instead.
-__device__ __forceinline__ long long div_up_to_64(long long a, long long b) {  // a >= 0, b > 0; mostly 32 bits
-  if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
-  return a / b;
-}
+// instead. Places on the line fit 31 bits (the host sees to it).
 struct Share {
-  long long line;   // units of a kv head
-  long long tiles;  // tiles of a kv head
-  long long ctas;   // B
-  bool whole;       // a tile a CTA
-  __device__ __forceinline__ long long start(const PageAttnArgs& a, long long b) const {
-    return whole ? b : div_up_to_64(line * a.c.nkv * b, ctas);
+  int line;    // units of a kv head (whole: its tiles)
+  int ctas;    // B
+  int q, r;    // total = q * B + r
+  bool whole;  // a tile a CTA
+  __device__ __forceinline__ int start(int b) const {
+    return whole ? b : q * b + static_cast<int>(static_cast<unsigned>(r * b) / static_cast<unsigned>(ctas));
   }
 };
+
+// One segment of a CTA's share: (part of) the keys of one tile.
 struct Segment {
-  int h, s, tile;  // kv head, stream, tile of it
-  int u, x0, x1;   // units of the tile, and the part of them
+  int h, s, tile;     // kv head, stream, tile of it
+  StreamRows q;       // the stream's rows
+  int u, x0, x1;      // units of the stream, and the part of them
+  int j_lo, j_hi;     // first and last row of the tile
+  int lo, lo_max, hi; // slots some row sees: from lo (all rows: from lo_max) to hi, and the sinks
+  int sinks;
+  UnitRange ur;       // the tile's units
+  int i0, i1;         // the segment's part of them
+};
+struct Run {
+  Share sh;
+  int at, end;
+  bool left;  // whether seg is one
+  Segment seg;
 };
 
-__device__ __forceinline__ int stream_units(const PageAttnArgs& a, int s, int* mt, bool flag) {
+// A lane's stream: its rows, tiles and units.
+struct LaneStream {
+  StreamRows q;
+  int mt, u;
+};
+__device__ __forceinline__ LaneStream lane_stream(const PageAttnArgs& a, int s, bool flag) {
+  LaneStream x{{0, 0, 0}, 0, 0};
+  if (s >= a.r.S) return x;
   bool bad;
-  const StreamRows q = stream_rows(a.r, s, &bad);
+  x.q = stream_rows(a.r, s, &bad);
   if (bad && flag) flag_status(a.r.status, DFLASH_STATUS_BAD_ROWS);
-  *mt = (q.n * a.G + (1 << a.tile_log2) - 1) >> a.tile_log2;  // max_rows * G is under 2^31
-  if (q.n == 0) return 0;
-  const int lo = a.window > 0 ? max(0, q.C - a.window + 1) : 0;
-  return unit_range(lo, q.C + q.n, a.sinks, a.unit_log2).n;
+  if (x.q.n == 0) return x;
+  x.mt = (x.q.n * a.G + (1 << a.tile_log2) - 1) >> a.tile_log2;  // max_rows * G is under 2^31
+  const int lo = a.window > 0 ? max(0, x.q.C - a.window + 1) : 0;
+  x.u = unit_range(lo, x.q.C + x.q.n, a.sinks, a.unit_log2).n;
+  return x;
 }
 
-// One warp; every lane gets the answer.
-__device__ __forceinline__ Share share_of(const PageAttnArgs& a) {
+// One warp; every lane gets the answer. `last`: the lanes' streams when there
+// are no more than 32 of them.
+__device__ __forceinline__ Share share_of(const PageAttnArgs& a, LaneStream& last) {
   const int lane = threadIdx.x & 31;
-  long long line = 0, tiles = 0;
+  unsigned line = 0, tiles = 0;
   int most = 0;
   for (int s0 = 0; s0 < a.r.S; s0 += 32) {
-    int mt = 0, u = 0;
-    if (s0 + lane < a.r.S) u = stream_units(a, s0 + lane, &mt, blockIdx.x == 0 && blockIdx.y == 0);
-    line += static_cast<long long>(mt) * u;
-    tiles += mt;
-    most = max(most, u);
+    last = lane_stream(a, s0 + lane, blockIdx.x == 0 && blockIdx.y == 0);
+    line += __reduce_add_sync(0xffffffffu, static_cast<unsigned>(last.mt * last.u));
+    tiles += __reduce_add_sync(0xffffffffu, static_cast<unsigned>(last.mt));
+    most = max(most, __reduce_max_sync(0xffffffffu, last.u));
   }
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
-    line += __shfl_xor_sync(0xffffffffu, line, o);
-    tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
-  }
-  most = __reduce_max_sync(0xffffffffu, most);
   Share sh;
-  sh.line = line;
-  sh.tiles = tiles;
-  sh.whole = a.part_o == nullptr || most <= a.no_split || tiles * a.c.nkv >= 3ll * a.target;
+  const unsigned all = tiles * a.c.nkv;
+  sh.whole = a.part_o == nullptr || most <= a.no_split || all >= 3u * a.target;
+  sh.q = sh.r = 0;
   if (sh.whole) {
-    sh.ctas = tiles * a.c.nkv;
+    sh.line = static_cast<int>(tiles);
+    sh.ctas = static_cast<int>(all);
   } else {
-    const long long b = div_up_to_64(line * a.c.nkv + a.min_units - 1, a.min_units);
-    sh.ctas = b < a.target ? b : a.target;
+    const unsigned total = line * a.c.nkv, b = (total + a.min_units - 1) / a.min_units;
+    sh.line = static_cast<int>(line);
+    sh.ctas = min(static_cast<int>(b), a.target);
+    sh.q = static_cast<int>(total / sh.ctas);
+    sh.r = static_cast<int>(total - sh.q * static_cast<unsigned>(sh.ctas));
   }
   return sh;
 }
 
-// The segment at place `at` of the line (whole: tile `at`), open to the tile's
-// end. One warp.
-__device__ __forceinline__ Segment segment_at(const PageAttnArgs& a, const Share& sh, long long at) {
-  const int lane = threadIdx.x & 31;
-  const long long per = sh.whole ? sh.tiles : sh.line;
-  Segment g;
-  g.h = static_cast<int>(div_up_to_64(at, per));
-  const long long r = at - g.h * per;
-  long long base = 0;
-  g.s = g.tile = g.u = g.x0 = g.x1 = 0;
-  for (int s0 = 0; s0 < a.r.S; s0 += 32) {
-    int mt = 0, u = 0;
-    if (s0 + lane < a.r.S) u = stream_units(a, s0 + lane, &mt, false);
-    const long long cnt = sh.whole ? mt : static_cast<long long>(mt) * u;
-    long long inc = cnt;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += x;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, r < base + inc);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      const long long rel = r - base - __shfl_sync(0xffffffffu, inc - cnt, l);
-      g.s = s0 + l;
-      g.u = __shfl_sync(0xffffffffu, u, l);
-      const int tiles = __shfl_sync(0xffffffffu, mt, l);
-      const int tile = static_cast<int>(sh.whole ? rel : div_up_to_64(rel, g.u));
-      g.x0 = sh.whole ? 0 : static_cast<int>(rel - static_cast<long long>(tile) * g.u);
-      g.x1 = g.u;
-      g.tile = tiles - 1 - tile;  // the last rows see most: whole tiles start with them
-      return g;
-    }
-    base += __shfl_sync(0xffffffffu, inc, 31);
-  }
-  return g;
+__device__ __forceinline__ int row_pos(const RowsArgs& r, const StreamRows& q, int j) {
+  return q.C + (r.depth ? max(0, min(r.depth[q.row0 + j], 0x3fffffff)) : j);
 }
 
-// A CTA's run of segments, kept in shared memory between them.
-struct Run {
-  Share sh;
-  long long at, end;
-  Segment seg;
-  int left;  // whether seg is one
-};
-__device__ __forceinline__ void run_begin(const PageAttnArgs& a, Run* run) {
-  const Share sh = share_of(a);
-  if ((threadIdx.x & 31) == 0) {
-    const bool on = blockIdx.x < sh.ctas;
-    run->sh = sh;
-    run->at = on ? sh.start(a, blockIdx.x) : 0;
-    run->end = on ? sh.start(a, blockIdx.x + 1ll) : 0;
+// The segment at place `at` of the line, `left` units (whole: a tile) at most.
+// One warp; false past the end. known: the lanes' streams, if they are at hand.
+__device__ __forceinline__ bool segment_at(const PageAttnArgs& a, const Share& sh, int at, int left,
+                                           bool have, const LaneStream& known, Segment* out) {
+  const int lane = threadIdx.x & 31;
+  Segment g;
+  g.h = static_cast<int>(static_cast<unsigned>(at) / static_cast<unsigned>(sh.line));
+  const int r = at - g.h * sh.line;
+  int base = 0;
+  for (int s0 = 0; s0 < a.r.S; s0 += 32) {
+    const LaneStream x = have ? known : lane_stream(a, s0 + lane, false);
+    const int cnt = sh.whole ? x.mt : x.mt * x.u;
+    int inc = cnt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, r < base + inc);
+    if (!hit) {
+      base += __shfl_sync(0xffffffffu, inc, 31);
+      continue;
+    }
+    const int l = __ffs(hit) - 1;
+    const int rel = r - base - __shfl_sync(0xffffffffu, inc - cnt, l);
+    g.s = s0 + l;
+    g.u = __shfl_sync(0xffffffffu, x.u, l);
+    g.q.row0 = __shfl_sync(0xffffffffu, x.q.row0, l);
+    g.q.n = __shfl_sync(0xffffffffu, x.q.n, l);
+    g.q.C = __shfl_sync(0xffffffffu, x.q.C, l);
+    const int tiles = __shfl_sync(0xffffffffu, x.mt, l);
+    const int tile = sh.whole ? rel : static_cast<int>(static_cast<unsigned>(rel) / static_cast<unsigned>(g.u));
+    g.x0 = sh.whole ? 0 : rel - tile * g.u;
+    g.x1 = sh.whole ? g.u : min(g.u, g.x0 + left);
+    g.tile = tiles - 1 - tile;  // the last rows see most: whole tiles start with them
+    const unsigned f0 = static_cast<unsigned>(g.tile) << a.tile_log2;
+    g.j_lo = static_cast<int>(f0 / static_cast<unsigned>(a.G));
+    g.j_hi = min(g.q.n - 1, static_cast<int>((f0 + (1u << a.tile_log2) - 1u) / static_cast<unsigned>(a.G)));
+    g.hi = g.q.C + (a.mode == DFLASH_MASK_CAUSAL ? g.j_hi + 1 : g.q.n);
+    g.sinks = min(a.sinks, g.hi);
+    g.lo = g.lo_max = 0;
+    if (a.window > 0) {
+      int p_lo = g.q.C + g.j_lo, p_hi = g.q.C + g.j_hi;
+      if (a.r.depth) {
+        p_lo = 0x7fffffff;
+        p_hi = 0;
+        for (int j = g.j_lo + lane; j <= g.j_hi; j += 32) {
+          const int p = row_pos(a.r, g.q, j);
+          p_lo = min(p_lo, p);
+          p_hi = max(p_hi, p);
+        }
+        p_lo = __reduce_min_sync(0xffffffffu, p_lo);
+        p_hi = __reduce_max_sync(0xffffffffu, p_hi);
+      }
+      g.lo = min(g.q.C, max(0, p_lo - a.window + 1));
+      g.lo_max = max(0, p_hi - a.window + 1);
+    }
+    g.ur = unit_range(g.lo, g.hi, a.sinks, a.unit_log2);
+    g.i0 = 0;
+    g.i1 = g.ur.n;
+    // a tile's own units in the stream's proportion
+    if (g.x0 > 0 || g.x1 < g.u) {
+      const bool same = g.ur.n == g.u;
+      g.i0 = same ? g.x0 : static_cast<int>(static_cast<long long>(g.ur.n) * g.x0 / g.u);
+      g.i1 = same ? g.x1 : static_cast<int>(static_cast<long long>(g.ur.n) * g.x1 / g.u);
+    }
+    *out = g;
+    return true;
   }
-  __syncwarp();
+  return false;
 }
-__device__ __forceinline__ void run_next(const PageAttnArgs& a, Run* run) {
-  const long long at = run->at, left = run->end - at;
-  Segment sg{};
-  if (left > 0) {
-    const Share sh = run->sh;
-    sg = segment_at(a, sh, at);
-    if (!sh.whole && sg.x1 - sg.x0 > left) sg.x1 = sg.x0 + static_cast<int>(left);
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) run->at = at + (sh.whole ? 1 : sg.x1 - sg.x0);
+
+// The CTA's next segment into run->seg. One warp.
+__device__ __forceinline__ void run_next(const PageAttnArgs& a, Run* run, bool begin) {
+  const bool one = (threadIdx.x & 31) == 0;
+  Share sh;
+  LaneStream x{{0, 0, 0}, 0, 0};
+  int at = 0, end = 0;
+  if (begin) {
+    sh = share_of(a, x);
+    if (static_cast<int>(blockIdx.x) < sh.ctas) {
+      at = sh.start(static_cast<int>(blockIdx.x));
+      end = sh.start(static_cast<int>(blockIdx.x) + 1);
+    }
+    if (one) {
+      run->sh = sh;
+      run->end = end;
+    }
+  } else {
+    sh = run->sh;
+    at = run->at;
+    end = run->end;
   }
-  if ((threadIdx.x & 31) == 0) {
-    run->seg = sg;
-    run->left = left > 0;
-  }
+  Segment g;
+  const bool left = at < end && segment_at(a, sh, at, end - at, begin && a.r.S <= 32, x, &g);
   __syncwarp();
+  if (one) {
+    run->left = left;
+    if (left) {
+      run->seg = g;
+      run->at = at + (sh.whole ? 1 : g.x1 - g.x0);
+    }
+  }
 }
 
 // What one (query row, head) pair of a tile sees.
@@ -227,10 +280,6 @@ struct RowView {
   int pos;     // its position
   int back;    // first slot its window reaches (context part)
 };
-
-__device__ __forceinline__ int row_pos(const RowsArgs& r, const StreamRows& q, int j) {
-  return q.C + (r.depth ? max(0, min(r.depth[q.row0 + j], 0x3fffffff)) : j);
-}
 
 // Whether row v sees slot `slot` of its stream.
 __device__ __forceinline__ bool sees(const PageAttnArgs& a, const StreamRows& q, const RowView& v, int slot) {
