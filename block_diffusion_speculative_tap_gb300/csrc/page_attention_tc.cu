@@ -39,7 +39,9 @@ namespace {
 constexpr int kTK = 128;                 // keys a tile
 constexpr int kMRows = 128;              // rows of a softmax stream
 constexpr float kRescale = 8.f;          // log2 by which the maximum in use may lag
-constexpr int kSoftThreads = 256;
+constexpr int kSoftWarps = 16;           // two streams x two halves of the keys x four lane quadrants
+constexpr int kSoftThreads = 32 * kSoftWarps;
+constexpr int kMma = kSoftWarps;         // the MMA warp; the producers follow
 
 template <int D, bool FP4, bool PAIR>
 struct TcGeo {
@@ -55,7 +57,8 @@ struct TcGeo {
   static constexpr int kOffSlots = kQ;
   static constexpr int kOffRaw = kOffSlots + kSlots * kSlot;
   static constexpr int kOffBar = kOffRaw + kStage * kRaw;
-  static constexpr int kSmem = kOffBar + 512 + 1024;
+  static constexpr int kOffXch = kOffBar + 512;             // [2 streams][2 halves][128] fp32
+  static constexpr int kSmem = kOffXch + 2048;
   static constexpr int kPartLd = D + 4;
   static constexpr int kColO = 256;
   static constexpr float kShift = FP4 ? 7.f : 0.f;  // P <= 2^(kRescale + kShift) in fp16
@@ -68,15 +71,12 @@ struct TcPageArgs {
   PageAttnArgs a;
 };
 
-__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t lbo) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
-}
+// Shared-memory matrix descriptors by their low words: start address >> 4 (a
+// tile's address plus an offset: no carry leaves the field) and the leading
+// byte offset >> 4 at bit 16; the high word (stride 1024 bytes, version 1,
+// 128-byte swizzle) is the same for all.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo16) { return (saddr >> 4) | (lbo16 << 16); }
 
 // kind::f16 with fp16 (or bf16) A and B, fp32 accumulator; bit 16: B MN-major.
 constexpr uint32_t idesc16(bool half, int M, int N, bool b_mn) {
@@ -84,13 +84,24 @@ constexpr uint32_t idesc16(bool half, int M, int N, bool b_mn) {
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-__device__ __forceinline__ void umma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                        uint32_t accumulate) {
+// D (+)= A B^T with A in shared memory, and with A in tensor memory; one thread.
+template <bool ACC>
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(alo), "r"(blo), "r"(idesc), "n"(ACC ? 1 : 0), "n"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(blo), "r"(idesc), "r"(acc), "n"(kDescHi)
       : "memory");
 }
 
@@ -113,14 +124,12 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -163,6 +172,31 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return c;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Two fp32 values in one register pair: one instruction for both.
+__device__ __forceinline__ uint64_t two(float lo, float hi) {
+  uint64_t x;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(lo), "f"(hi));
+  return x;
+}
+__device__ __forceinline__ void untwo(uint64_t x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // Bits i of the 32 slots from `base` on with lo <= base + i < hi.
 __device__ __forceinline__ uint32_t range_bits(int lo, int hi, int base) {
   const int a = max(lo - base, 0), b = min(hi - base, 32);
@@ -176,8 +210,12 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
   using Ge = TcGeo<D, FP4, PAIR>;
   constexpr int kSlots = Ge::kSlots;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = smem_raw;  // the only shared memory of the kernel: swizzled tiles need its 1024-byte alignment
   const uint32_t sbase = smem_u32(smem);
+  if (sbase & 1023u) {
+    if (threadIdx.x == 0) flag_status(P.a.r.status, DFLASH_STATUS_TIMEOUT);
+    return;
+  }
   const PageAttnArgs& a = P.a;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Ge::kOffBar);  // [kSlots] a tile is in its slot
   uint64_t* empty = full + kSlots;   // [kSlots] the MMAs that read the slot are done
@@ -185,7 +223,8 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
   uint64_t* p_full = s_full + 2;     // [2] its weights are, and its output is rescaled
   uint64_t* q_full = p_full + 2;     // the queries are in shared memory
   uint64_t* o_full = q_full + 1;     // every MMA is done
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 1);
+  uint64_t* landed = o_full + 1;     // a tile that has to be cleaned is in its slot
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(landed + 1);
   int* abort_word = reinterpret_cast<int*>(tmem_slot + 1);
   Run* run = reinterpret_cast<Run*>(smem + Ge::kOffBar + 256);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -197,7 +236,7 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
   // between segments everything asynchronous has completed: the barriers start
   // again at phase 0
   if (warp == 0) run_next(a, run, first);
-  if (first && warp == 8) {
+  if (first && warp == kMma) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
@@ -208,10 +247,11 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], kMRows);
+      mbar_init(&p_full[s], kSoftWarps / 2);
     }
-    mbar_init(q_full, PAIR ? 2 * kMRows : kMRows);
+    mbar_init(q_full, PAIR ? kSoftWarps : kSoftWarps / 2);
     mbar_init(o_full, 1);
+    mbar_init(landed, 1);
     if (first) *abort_word = 0;
     fence_barrier_init();
   }
@@ -262,129 +302,111 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
     }
   };
 
-  if (warp == 8) {
-    // ------------------------------------------------ MMA issuer
-    constexpr uint32_t kIdS = idesc16(FP4, kMRows, kTK, false);
-    constexpr uint32_t kIdO = idesc16(FP4, kMRows, D, true);
-    bool ok = nt > 0 && mbar_wait(q_full, 0, err, DFLASH_STATUS_TIMEOUT, abort_word);
-    ok = __all_sync(0xffffffffu, ok);
-    bool any = false;
-    int e = 0;  // next ring entry
-    auto wait_entry = [&]() -> int {
-      const int sl = e % kSlots;
-      ok = ok && mbar_wait(&full[sl], (e / kSlots) & 1, err, DFLASH_STATUS_TIMEOUT, abort_word);
-      ok = __all_sync(0xffffffffu, ok);
-      ++e;
-      return sl;
-    };
-    auto scores = [&](int s, int sl) {
-      if (lane != 0) return;
-      tc_fence_after();
-      const uint32_t kb = sbase + Ge::kOffSlots + sl * Ge::kSlot;
-      const uint32_t qb = sbase + (PAIR ? s * kMRows * D * 2 : 0);
+  if (warp == kMma) {
+    // ------------------------------------------------ MMA issuer: one thread, and little code:
+    // whatever it does between MMAs the tensor cores stand still for
+    if (lane == 0) {
+      constexpr uint32_t kIdS = idesc16(FP4, kMRows, kTK, false);
+      constexpr uint32_t kIdO = idesc16(FP4, kMRows, D, true);
+      const uint32_t q_lo = desc_lo(sbase, 1), slots = sbase + Ge::kOffSlots;
+      bool ok = nt > 0 && mbar_wait(q_full, 0, err, DFLASH_STATUS_TIMEOUT, abort_word);
+      bool any = false;
+      int slot = 0;        // next ring slot, and the parity of its phase
+      uint32_t phase = 0;
+      auto wait_entry = [&]() -> int {
+        const int sl = slot;
+        ok = mbar_wait(&full[sl], phase, err, DFLASH_STATUS_TIMEOUT, abort_word);
+        if (++slot == kSlots) {
+          slot = 0;
+          phase ^= 1u;
+        }
+        return sl;
+      };
+      auto scores = [&](int s, int sl) {
+        tc_fence_after();
+        const uint32_t k_lo = desc_lo(slots + sl * Ge::kSlot, 1), a_lo = q_lo + (PAIR ? s * (kMRows * D * 2 >> 4) : 0);
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = (kk >> 2) * Ge::kSub + (kk & 3) * 32;
-        umma_bf16(tmem + s * 128, sdesc_sw128(qb + off), sdesc_sw128(kb + off), kIdS, kk > 0 ? 1u : 0u);
-      }
-      any = true;
-      umma_commit(&s_full[s]);
-    };
-    auto output = [&](int s, int sl, bool first) {
-      if (lane != 0) return;
-      tc_fence_after();
-      const uint32_t vb = sbase + Ge::kOffSlots + sl * Ge::kSlot;
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * Ge::kSub + (kk & 3) * 32) >> 4;
+          if (kk == 0) mma_ss<false>(tmem + s * 128, a_lo, k_lo, kIdS);
+          else mma_ss<true>(tmem + s * 128, a_lo + off, k_lo + off, kIdS);
+        }
+        any = true;
+        umma_commit(&s_full[s]);
+      };
+      auto output = [&](int s, int sl, bool first_tile) {
+        tc_fence_after();
+        const uint32_t v_lo = desc_lo(slots + sl * Ge::kSlot, Ge::kSub >> 4);
 #pragma unroll
-      for (int kk = 0; kk < kTK / 16; ++kk)
-        umma_ta(tmem + Ge::kColO + s * D, tmem + s * 128 + kk * 8, sdesc_mn(vb + kk * 16 * 128, Ge::kSub), kIdO,
-                (!first || kk > 0) ? 1u : 0u);
-    };
-    auto release = [&](int sl) {
-      if (lane == 0) umma_commit(&empty[sl]);
-    };
-    // V rows no row sees: whatever the slots hold, they count as zero (4-bit
-    // tiles are written clean)
-    auto clean = [&](int sl, int kb) {
-      if constexpr (FP4) return;
-      if (inside(kb)) return;
-      for (int r = 0; r < kTK; ++r) {
-        if (live(kb + r)) continue;
-        uint8_t* row = smem + Ge::kOffSlots + sl * Ge::kSlot + r * 128;
-        if (lane < D / 8)
-          *reinterpret_cast<uint4*>(row + (lane >> 3) * Ge::kSub + (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-      }
-      fence_async();
-      __syncwarp();
-    };
-    auto wait_p = [&](int s, int u) {
-      ok = ok && mbar_wait(&p_full[s], u & 1, err, DFLASH_STATUS_TIMEOUT, abort_word);
-      ok = __all_sync(0xffffffffu, ok);
-    };
-    if (PAIR) {
-      if (ok) {
-        const int sl = wait_entry();
+        for (int kk = 0; kk < kTK / 16; ++kk)
+          mma_ts(tmem + Ge::kColO + s * D, tmem + s * 128 + (kk >> 2) * 64 + (kk & 3) * 8, v_lo + kk * (16 * 128 >> 4),
+                 kIdO, !first_tile || kk > 0);
+      };
+      auto wait_p = [&](int s, int u) {
+        ok = mbar_wait(&p_full[s], u & 1, err, DFLASH_STATUS_TIMEOUT, abort_word);
+      };
+      if (PAIR) {
         if (ok) {
-          scores(0, sl);
-          scores(1, sl);
-          release(sl);
+          const int sl = wait_entry();
+          if (ok) {
+            scores(0, sl);
+            scores(1, sl);
+            umma_commit(&empty[sl]);
+          }
         }
-      }
-      for (int t = 0; t < nt && ok; ++t) {
-        int vs = 0, ks = 0;
-        wait_p(0, t);
-        if (ok) vs = wait_entry();
-        if (!ok) break;
-        clean(vs, slot0(t));
-        output(0, vs, t == 0);
-        if (t + 1 < nt) {
-          ks = wait_entry();
+#pragma unroll 1
+        for (int t = 0; t < nt && ok; ++t) {
+          const bool more = t + 1 < nt;
+          int ks = 0;
+          const int vs = wait_entry();
+          if (ok && more) ks = wait_entry();
           if (!ok) break;
-          scores(0, ks);
+#pragma unroll 1
+          for (int s = 0; s < 2; ++s) {
+            wait_p(s, t);
+            if (!ok) break;
+            output(s, vs, t == 0);
+            if (s == 1) umma_commit(&empty[vs]);
+            if (more) scores(s, ks);
+          }
+          if (ok && more) umma_commit(&empty[ks]);
         }
-        wait_p(1, t);
-        if (!ok) break;
-        output(1, vs, t == 0);
-        release(vs);
-        if (t + 1 < nt) {
-          scores(1, ks);
-          release(ks);
-        }
-      }
-    } else {
-      for (int t = 0; t < 2 && t < nt && ok; ++t) {
-        if (nt < 2 && t > 0) break;
-        const int sl = wait_entry();
-        if (!ok) break;
-        scores(t, sl);
-        release(sl);
-      }
-      for (int t = 0; t < nt && ok; ++t) {
-        const int s = t & 1;
-        wait_p(s, t >> 1);
-        if (!ok) break;
-        const int vs = wait_entry();
-        if (!ok) break;
-        clean(vs, slot0(t));
-        output(s, vs, t < 2);
-        release(vs);
-        if (t + 2 < nt) {
-          const int ks = wait_entry();
+      } else {
+#pragma unroll 1
+        for (int t = 0; t < 2 && t < nt && ok; ++t) {
+          const int sl = wait_entry();
           if (!ok) break;
-          scores(s, ks);
-          release(ks);
+          scores(t, sl);
+          umma_commit(&empty[sl]);
+        }
+#pragma unroll 1
+        for (int t = 0; t < nt && ok; ++t) {
+          const int s = t & 1, vs = wait_entry();
+          if (ok) wait_p(s, t >> 1);
+          if (!ok) break;
+          output(s, vs, t < 2);
+          umma_commit(&empty[vs]);
+          if (t + 2 < nt) {
+            const int ks = wait_entry();
+            if (!ok) break;
+            scores(s, ks);
+            umma_commit(&empty[ks]);
+          }
         }
       }
-    }
-    // every MMA completes before tensor memory is read for the last time or released
-    if (lane == 0 && any) {
-      umma_commit(o_full);
-      mbar_wait(o_full, 0, err, DFLASH_STATUS_TIMEOUT, nullptr);
+      // every MMA completes before tensor memory is read for the last time or released
+      if (any) {
+        umma_commit(o_full);
+        mbar_wait(o_full, 0, err, DFLASH_STATUS_TIMEOUT, nullptr);
+      }
     }
     __syncwarp();
-  } else if (warp > 8 && !FP4) {
+  } else if (warp > kMma && !FP4) {
     // ------------------------------------------------ TMA producer: a lane a box
     const int boxes = kTK / a.c.page;  // boxes of 64 dims a tile: boxes * D / 64 <= 16
+    const int b = lane % boxes, half = lane / boxes;
     int issued = 0;
+    uint32_t cleaned = 0;
     for (int e = 0; e < entries; ++e) {
       const int sl = e % kSlots;
       bool ok = e < kSlots || mbar_wait(&empty[sl], ((e / kSlots) & 1) ^ 1u, err, DFLASH_STATUS_TIMEOUT, abort_word);
@@ -393,27 +415,43 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
       int kv, t;
       entry(e, &kv, &t);
       const int kb = slot0(t);
-      const int b = lane % boxes, half = lane / boxes;
       const int slot = kb + b * a.c.page;
       const bool need = half < D / 64 && ((slot < hi && slot + a.c.page > lo) || slot < sinks);
       const int pg = need ? page_of(slot) : -1;
       if (need && pg < 0) flag_status(err, DFLASH_STATUS_BAD_PAGE);
       const unsigned go = __ballot_sync(0xffffffffu, pg >= 0);
-      if (lane == 0) mbar_arrive_expect_tx(&full[sl], __popc(go) * a.c.page * 128);
+      // V rows that no row sees count as zero whatever their slots hold: such a
+      // tile lands on a barrier of its own and is handed on once they are
+      // cleared (the first and last tile of a segment at most, and the sinks')
+      const bool edge = kv && !inside(kb);
+      uint64_t* bar = edge ? landed : &full[sl];
+      uint8_t* tile = smem + Ge::kOffSlots + sl * Ge::kSlot;
+      if (lane == 0) mbar_arrive_expect_tx(bar, __popc(go) * a.c.page * 128);
       __syncwarp();
       if (pg >= 0)
-        tma_tile(sbase + Ge::kOffSlots + sl * Ge::kSlot + half * Ge::kSub + b * a.c.page * 128,
-                 kv ? &P.vmap : &P.kmap, &full[sl], half * 64, (pg * a.c.nkv + h) * a.c.page);
+        tma_tile(smem_u32(tile) + half * Ge::kSub + b * a.c.page * 128, kv ? &P.vmap : &P.kmap, bar, half * 64,
+                 (pg * a.c.nkv + h) * a.c.page);
       issued = e + 1;
+      if (edge) {
+        ok = mbar_wait(landed, cleaned, err, DFLASH_STATUS_TIMEOUT, nullptr);
+        cleaned ^= 1u;
+        for (int r = 0; r < kTK; ++r)
+          if (!live(kb + r) && lane < D / 8)
+            *reinterpret_cast<uint4*>(tile + r * 128 + (lane >> 3) * Ge::kSub + (lane & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+        fence_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[sl]);
+      }
     }
     // no copy may still be landing when the slots are used again below
     for (int e = max(0, issued - kSlots); e < issued; ++e)
       mbar_wait(&full[e % kSlots], (e / kSlots) & 1, err, DFLASH_STATUS_TIMEOUT, nullptr);
-  } else if (FP4 && warp > 8) {
+  } else if (FP4 && warp > kMma) {
     // ------------------------------------------------ 4-bit producers: a thread a key
     if constexpr (FP4) {
     constexpr int kSt = Ge::kStage;
-    const int key = threadIdx.x - (kSoftThreads + 32);
+    const int key = static_cast<int>(threadIdx.x) - (kSoftThreads + 32);
     const uint32_t raw_u = sbase + Ge::kOffRaw + key * Ge::kRow;
     const uint8_t* raw = smem + Ge::kOffRaw + key * Ge::kRow;
     constexpr int kPieces = Ge::kRow / 16;
@@ -488,10 +526,16 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
     }
   } else {
     // ------------------------------------------------ softmax streams
-    const int s = warp >> 2, q4 = warp & 3;
+    // two warps a lane quadrant of a stream: each takes 64 keys of a tile (and
+    // half of the output's columns) of the quadrant's 32 rows, a thread a row.
+    // P lies over the warp's own scores, so the halves never wait for each
+    // other but to share a row's maximum.
+    const int s = warp >> 3, half = (warp >> 2) & 1, q4 = warp & 3;
     const int r = q4 * 32 + lane;
+    const int pair_bar = 1 + s * 4 + q4;
     const uint32_t tl = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
-    const uint32_t ts = tl + s * 128, to = tl + Ge::kColO + s * D;
+    const uint32_t ts = tl + s * 128 + half * 64, to = tl + Ge::kColO + s * D + half * (D / 2);
+    float* xch = reinterpret_cast<float*>(smem + Ge::kOffXch) + s * 256;
     const unsigned f = f0 + (PAIR ? s * kMRows : 0) + r;
     RowView rv;
     const int jr = static_cast<int>(f / a.G);
@@ -501,13 +545,12 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
     rv.back = a.window > 0 ? max(0, rv.pos - a.window + 1) : 0;
     const bool idle = __all_sync(0xffffffffu, rv.j < 0);  // a warp of padding rows takes no part
     float sc = a.scale;
-    if (PAIR || s == 0) {
-      // this thread's query row, swizzled as TMA would write it
+    {
       const __nv_bfloat16* src =
           rv.j >= 0 ? a.q + static_cast<int64_t>(q.row0 + jr) * a.q_ld + (h * a.G + hd) * D : nullptr;
-      uint8_t* dst = smem + (PAIR ? s * kMRows * D * 2 : 0) + r * 128;
       float down = 1.f;
       if (FP4) {
+        // into fp16 over a power of two a row
         float top = 0.f;
         if (src)
           for (int c = 0; c < D / 8; ++c) {
@@ -521,47 +564,49 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
         down = ldexpf(1.f, -ex);
         sc *= ldexpf(1.f, ex);
       }
+      if (PAIR || s == 0) {
+        // this thread's half of a query row, swizzled as TMA would write it
+        uint8_t* dst = smem + (PAIR ? s * kMRows * D * 2 : 0) + r * 128;
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        uint4 w = src ? reinterpret_cast<const uint4*>(src)[c] : make_uint4(0u, 0u, 0u, 0u);
-        if (FP4) {
-          uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        for (int c0 = 0; c0 < D / 16; ++c0) {
+          const int c = half * (D / 16) + c0;
+          uint4 w = src ? reinterpret_cast<const uint4*>(src)[c] : make_uint4(0u, 0u, 0u, 0u);
+          if (FP4) {
+            uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            u[x] = pack2<true>(__uint_as_float(u[x] << 16) * down, __uint_as_float(u[x] & 0xffff0000u) * down);
-          w = make_uint4(u[0], u[1], u[2], u[3]);
+            for (int x = 0; x < 4; ++x)
+              u[x] = pack2<true>(__uint_as_float(u[x] << 16) * down, __uint_as_float(u[x] & 0xffff0000u) * down);
+            w = make_uint4(u[0], u[1], u[2], u[3]);
+          }
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * Ge::kSub + (((c & 7) ^ (r & 7)) << 4)) = w;
         }
-        *reinterpret_cast<uint4*>(dst + (c >> 3) * Ge::kSub + (((c & 7) ^ (r & 7)) << 4)) = w;
+        fence_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
       }
-      fence_async();
-      mbar_arrive(q_full);
-    }
-    if (FP4 && !PAIR) {
-      // both streams scale a row's scores alike
-      float* scs = reinterpret_cast<float*>(smem + Ge::kOffBar + 512);
-      if (s == 0) scs[r] = sc;
-      named_bar_sync(1, kSoftThreads);
-      sc = scs[r];
     }
     float m = -INFINITY, l = 0.f;
     const int n_mine = PAIR ? nt : (nt + 1 - s) / 2;
     bool ok = true;
     for (int u = 0; u < n_mine; ++u) {
-      ok = mbar_wait(&s_full[s], u & 1, err, DFLASH_STATUS_TIMEOUT, abort_word);
+      // (the two warps of a quadrant meet at a named barrier below: a wait that
+      // gives up in one of them must not leave the other there, so after a
+      // failure both go on to the barrier and stop behind it)
+      if (ok) ok = mbar_wait(&s_full[s], u & 1, err, DFLASH_STATUS_TIMEOUT, abort_word);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
       if (idle) {
-        mbar_arrive(&p_full[s]);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(&p_full[s]);
         continue;
       }
       tc_fence_after();
       const int kb = slot0(PAIR ? u : 2 * u + s);
       const bool whole = kb + kTK <= all_end && (kb >= lo_max || kb + kTK <= sinks);
-      uint32_t vis[4];
+      uint32_t vis[2];
       if (!whole) {
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const int base = kb + 32 * w;
+        for (int w = 0; w < 2; ++w) {
+          const int base = kb + half * 64 + 32 * w;
           uint32_t b;
           if (plain) {
             const int end = a.mode == DFLASH_MASK_CAUSAL ? q.C + rv.j + 1 : q.C + q.n;
@@ -589,32 +634,40 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
           vis[w] = rv.j >= 0 ? b : 0u;
         }
       }
-      // the row's largest score of the tile; 64 scores at a time, read again
-      // for the weights (128 held across would spill)
+      // the row's largest score of the tile
       float sv[64];
       auto load_scores = [&](int c) {
-        tmem_ld32(ts + c * 64, reinterpret_cast<uint32_t*>(sv));
-        tmem_ld32(ts + c * 64 + 32, reinterpret_cast<uint32_t*>(sv) + 32);
-        tmem_wait_ld();
+        tmem_ld32(ts + c * 32, reinterpret_cast<uint32_t*>(sv) + c * 32);
+      };
+      auto hide = [&](int c) {
         if (!whole) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (!((vis[c * 2 + (i >> 5)] >> (i & 31)) & 1u)) sv[i] = -INFINITY;
+          for (int i = 0; i < 32; ++i)
+            if (!((vis[c] >> i) & 1u)) sv[c * 32 + i] = -INFINITY;
         }
       };
-      float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
+      load_scores(0);
+      load_scores(1);
+      tmem_wait_ld();
+      hide(0);
+      hide(1);
+      float t0 = sv[0], t1 = sv[1], t2 = sv[2], t3 = sv[3];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        load_scores(c);
-#pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          t0 = fmaxf(t0, sv[i]);
-          t1 = fmaxf(t1, sv[i + 1]);
-          t2 = fmaxf(t2, sv[i + 2]);
-          t3 = fmaxf(t3, sv[i + 3]);
-        }
+      for (int i = 4; i < 60; i += 8) {
+        t0 = max3(t0, sv[i], sv[i + 1]);
+        t1 = max3(t1, sv[i + 2], sv[i + 3]);
+        t2 = max3(t2, sv[i + 4], sv[i + 5]);
+        t3 = max3(t3, sv[i + 6], sv[i + 7]);
       }
-      const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * sc;
+      float top = max3(max3(t0, sv[60], sv[61]), max3(t1, sv[62], sv[63]), fmaxf(t2, t3));
+      // the other half's maximum; its last value has been read before its scores
+      // of this tile could be issued
+      xch[half * 128 + r] = top;
+      if (named_bar_or(pair_bar, 64, ok ? 0 : 1)) {
+        ok = false;
+        break;
+      }
+      top = fmaxf(top, xch[(half ^ 1) * 128 + r]) * sc;
       // The scores are complete, so every output product before them is too:
       // the output may be rescaled in place.
       const bool need = top > m + kRescale;
@@ -624,42 +677,42 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
         if (u > 0) {
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
-            float v[32];
-            tmem_ld32(to + c * 32, reinterpret_cast<uint32_t*>(v));
-            tmem_wait_ld();
+            float v[16];
+            tmem_ld16(to + c * 16, v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] *= alpha;
-            tmem_st32(to + c * 32, reinterpret_cast<uint32_t*>(v));
+            for (int i = 0; i < 16; ++i) v[i] *= alpha;
+            tmem_st16(to + c * 16, reinterpret_cast<const uint32_t*>(v));
           }
         }
         if (need) m = top;
       }
       const float neg = m == -INFINITY ? 0.f : Ge::kShift - m;
-      float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+      const uint64_t sc2 = two(sc, sc), neg2 = two(neg, neg);
+      uint64_t sum0 = 0ull, sum1 = 0ull;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        uint32_t pk[32];  // columns 32c ..: scores read already
-        load_scores(c);
+        uint32_t pk[16];
 #pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          float* x = sv + i;
-          x[0] = ex2f(fmaf(x[0], sc, neg));
-          x[1] = ex2f(fmaf(x[1], sc, neg));
-          x[2] = ex2f(fmaf(x[2], sc, neg));
-          x[3] = ex2f(fmaf(x[3], sc, neg));
-          a0 += x[0];
-          a1 += x[1];
-          a2 += x[2];
-          a3 += x[3];
+        for (int i = 0; i < 32; i += 4) {
+          float* x = sv + c * 32 + i;
+          untwo(fma2(two(x[0], x[1]), sc2, neg2), x[0], x[1]);
+          untwo(fma2(two(x[2], x[3]), sc2, neg2), x[2], x[3]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[k] = ex2f(x[k]);
+          sum0 = add2(sum0, two(x[0], x[1]));
+          sum1 = add2(sum1, two(x[2], x[3]));
           pk[i / 2] = pack2<FP4>(x[0], x[1]);
           pk[i / 2 + 1] = pack2<FP4>(x[2], x[3]);
         }
-        tmem_st32(ts + c * 32, pk);
+        tmem_st16(ts + c * 16, pk);
       }
-      l += (a0 + a1) + (a2 + a3);
+      float a0, a1;
+      untwo(add2(sum0, sum1), a0, a1);
+      l += a0 + a1;
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(&p_full[s]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[s]);
     }
     // ------------------------------------------------ output
     if (nt > 0) {
@@ -668,27 +721,32 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
       tc_fence_after();
     }
     const bool mine = ok && n_mine > 0 && !idle;
+    // a row's sum is its halves' sums
+    xch[half * 128 + r] = mine ? l : 0.f;
+    named_bar_sync(pair_bar, 64);
+    l = xch[r] + xch[128 + r];
     float* xo = reinterpret_cast<float*>(smem + Ge::kOffSlots);  // [128][kPartLd] the second stream's rows
     float* xm = xo + kMRows * Ge::kPartLd;                       // [128][2]
     float m1 = -INFINITY, l1 = 0.f;
     if (!PAIR) {
       if (s == 1) {
-        xm[2 * r] = mine ? m : -INFINITY;
-        xm[2 * r + 1] = mine ? l : 0.f;
+        if (half == 0) {
+          xm[2 * r] = mine ? m : -INFINITY;
+          xm[2 * r + 1] = mine ? l : 0.f;
+        }
         if (mine) {
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
-            float v[32];
-            tmem_ld32(to + c * 32, reinterpret_cast<uint32_t*>(v));
-            tmem_wait_ld();
+            float v[16];
+            tmem_ld16(to + c * 16, v);
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<float4*>(xo + r * Ge::kPartLd + c * 32 + i) =
+            for (int i = 0; i < 16; i += 4)
+              *reinterpret_cast<float4*>(xo + r * Ge::kPartLd + half * (D / 2) + c * 16 + i) =
                   make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
           }
         }
       }
-      named_bar_sync(1, kSoftThreads);
+      named_bar_sync(9, kSoftThreads);
       if (s == 0) {
         m1 = xm[2 * r];
         l1 = xm[2 * r + 1];
@@ -702,20 +760,22 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
       const float inv = split ? 1.f : M == -INFINITY ? 0.f : 1.f / den;
       const bool write = rv.j >= 0;
       const int64_t prow = part_row + (PAIR ? s * kMRows : 0) + r;
-      __nv_bfloat16* dst = a.out + static_cast<int64_t>(q.row0 + jr) * a.out_ld + (h * a.G + hd) * D;
+      __nv_bfloat16* dst = a.out + static_cast<int64_t>(q.row0 + jr) * a.out_ld + (h * a.G + hd) * D + half * (D / 2);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
-        float v[32];
+        float v[16];
         if (mine) {
-          tmem_ld32(to + c * 32, reinterpret_cast<uint32_t*>(v));
-          tmem_wait_ld();
+          tmem_ld16(to + c * 16, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = w0 > 0.f ? v[i] * w0 : 0.f;
+        for (int i = 0; i < 16; ++i) v[i] = w0 > 0.f ? v[i] * w0 : 0.f;
         if (!PAIR && w1 > 0.f) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 x = *reinterpret_cast<const float4*>(xo + r * Ge::kPartLd + c * 32 + i);
+          for (int i = 0; i < 16; i += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(xo + r * Ge::kPartLd + half * (D / 2) + c * 16 + i);
             v[i] = fmaf(x.x, w1, v[i]);
             v[i + 1] = fmaf(x.y, w1, v[i + 1]);
             v[i + 2] = fmaf(x.z, w1, v[i + 2]);
@@ -725,37 +785,35 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
         if (!write) continue;
         if (split) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(a.part_o + prow * D + c * 32 + i) =
+          for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<float4*>(a.part_o + prow * D + half * (D / 2) + c * 16 + i) =
                 make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8)
-            *reinterpret_cast<uint4*>(dst + c * 32 + i) =
+          for (int i = 0; i < 16; i += 8)
+            *reinterpret_cast<uint4*>(dst + c * 16 + i) =
                 make_uint4(pack2<false>(v[i] * inv, v[i + 1] * inv), pack2<false>(v[i + 2] * inv, v[i + 3] * inv),
                            pack2<false>(v[i + 4] * inv, v[i + 5] * inv), pack2<false>(v[i + 6] * inv, v[i + 7] * inv));
         }
       }
-      if (split && write) *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(M, den);
+      if (split && write && half == 0) *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(M, den);
     }
-    tc_fence_before();
   }
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 32) {
-    for (uint64_t* b = full; b <= o_full; ++b)
+    for (uint64_t* b = full; b <= landed; ++b)
       asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(b)) : "memory");
   }
   }
-  if (warp == 8) tmem_dealloc(*tmem_slot, 512);
+  if (warp == kMma) tmem_dealloc(*tmem_slot, 512);
 }
 
 template <int D, bool FP4, bool PAIR>
 int launch(const TcPageArgs& P, const PagePlan& p, cudaStream_t st) {
   using Ge = TcGeo<D, FP4, PAIR>;
   auto kern = page_attn_tc_kernel<D, FP4, PAIR>;
-  constexpr int kBytes = Ge::kSmem + (FP4 && !PAIR ? 512 : 0);
-  static_assert(kBytes <= 232448, "shared memory of an SM");
+  constexpr int kBytes = Ge::kSmem;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) != cudaSuccess) {
     cudaGetLastError();
     return DFLASH_E_CUDA;

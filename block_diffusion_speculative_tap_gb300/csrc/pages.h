@@ -175,8 +175,11 @@ __device__ __forceinline__ bool segment_at(const PageAttnArgs& a, const Share& s
                                            bool have, const LaneStream& known, Segment* out) {
   const int lane = threadIdx.x & 31;
   Segment g;
-  g.h = static_cast<int>(static_cast<unsigned>(at) / static_cast<unsigned>(sh.line));
-  const int r = at - g.h * sh.line;
+  // whole tiles: every head's longest first
+  const int quot = static_cast<int>(static_cast<unsigned>(at) / static_cast<unsigned>(sh.whole ? a.c.nkv : sh.line));
+  const int rest = at - quot * (sh.whole ? a.c.nkv : sh.line);
+  g.h = sh.whole ? rest : quot;
+  const int r = sh.whole ? quot : rest;
   int base = 0;
   for (int s0 = 0; s0 < a.r.S; s0 += 32) {
     const LaneStream x = have ? known : lane_stream(a, s0 + lane, false);
