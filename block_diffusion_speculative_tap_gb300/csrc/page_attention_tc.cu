@@ -405,8 +405,18 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
     // ------------------------------------------------ TMA producer: a lane a box
     const int boxes = kTK / a.c.page;  // boxes of 64 dims a tile: boxes * D / 64 <= 16
     const int b = lane % boxes, half = lane / boxes;
-    int issued = 0;
+    int issued = 0, k_tile = -1;
     uint32_t cleaned = 0;
+    // a lane's page of key tiles k_tile .. k_tile - 2 and, looked up ahead, k_tile + 1
+    auto lookup = [&](int t) -> int {
+      if (t >= nt) return -1;
+      const int slot = slot0(t) + b * a.c.page;
+      if (half >= D / 64 || !((slot < hi && slot + a.c.page > lo) || slot < sinks)) return -1;
+      const int pg = page_of(slot);
+      if (pg < 0) flag_status(err, DFLASH_STATUS_BAD_PAGE);
+      return pg;
+    };
+    int pgs[4] = {lookup(0), -1, -1, -1};
     for (int e = 0; e < entries; ++e) {
       const int sl = e % kSlots;
       bool ok = e < kSlots || mbar_wait(&empty[sl], ((e / kSlots) & 1) ^ 1u, err, DFLASH_STATUS_TIMEOUT, abort_word);
@@ -415,10 +425,14 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
       int kv, t;
       entry(e, &kv, &t);
       const int kb = slot0(t);
-      const int slot = kb + b * a.c.page;
-      const bool need = half < D / 64 && ((slot < hi && slot + a.c.page > lo) || slot < sinks);
-      const int pg = need ? page_of(slot) : -1;
-      if (need && pg < 0) flag_status(err, DFLASH_STATUS_BAD_PAGE);
+      if (!kv) {
+        k_tile = t;
+        pgs[3] = pgs[2];
+        pgs[2] = pgs[1];
+        pgs[1] = pgs[0];
+        pgs[0] = lookup(t + 1);
+      }
+      const int pg = t == k_tile ? pgs[1] : t == k_tile - 1 ? pgs[2] : pgs[3];
       const unsigned go = __ballot_sync(0xffffffffu, pg >= 0);
       // V rows that no row sees count as zero whatever their slots hold: such a
       // tile lands on a barrier of its own and is handed on once they are
