@@ -39,13 +39,13 @@ namespace {
 constexpr int kTK = 128;                 // keys a tile
 constexpr int kMRows = 128;              // rows of a softmax stream
 constexpr float kRescale = 8.f;          // log2 by which the maximum in use may lag
-constexpr int kSoftWarps = 16;           // two streams x two halves of the keys x four lane quadrants
+constexpr int kSoftWarps = 8;            // two streams x four lane quadrants
 constexpr int kSoftThreads = 32 * kSoftWarps;
 constexpr int kMma = kSoftWarps;         // the MMA warp; the producers follow
 
 template <int D, bool FP4, bool PAIR>
 struct TcGeo {
-  static constexpr int kProd = FP4 ? 4 : 1;                 // producer warps
+  static constexpr int kProd = FP4 ? 4 : 2;                 // producer warps (bf16: K, V)
   static constexpr int kThreads = kSoftThreads + 32 + 32 * kProd;
   static constexpr int kSub = kTK * 128;                    // 128 rows x 64 dims
   static constexpr int kSlot = kTK * D * 2;                 // a K or V tile
@@ -57,8 +57,8 @@ struct TcGeo {
   static constexpr int kOffSlots = kQ;
   static constexpr int kOffRaw = kOffSlots + kSlots * kSlot;
   static constexpr int kOffBar = kOffRaw + kStage * kRaw;
-  static constexpr int kOffXch = kOffBar + 512;             // [2 streams][2 halves][128] fp32
-  static constexpr int kSmem = kOffXch + 2048;
+  static constexpr int kSmem = kOffBar + 512;
+  static constexpr int kHold = FP4 ? 2 : 4;  // of a tile's four chunks of 32 scores, those kept in registers
   static constexpr int kPartLd = D + 4;
   static constexpr int kColO = 256;
   static constexpr float kShift = FP4 ? 7.f : 0.f;  // P <= 2^(kRescale + kShift) in fp16
@@ -302,6 +302,12 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
     }
   };
 
+  auto entry_of = [&](int kv, int t) {  // its inverse
+    if (PAIR || nt < 2) return 2 * t + kv;
+    if (kv) return t == nt - 1 ? entries - 1 : 2 * t + 2;
+    return t < 2 ? t : 2 * t - 1;
+  };
+
   if (warp == kMma) {
     // ------------------------------------------------ MMA issuer: one thread, and little code:
     // whatever it does between MMAs the tensor cores stand still for
@@ -339,7 +345,7 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
         const uint32_t v_lo = desc_lo(slots + sl * Ge::kSlot, Ge::kSub >> 4);
 #pragma unroll
         for (int kk = 0; kk < kTK / 16; ++kk)
-          mma_ts(tmem + Ge::kColO + s * D, tmem + s * 128 + (kk >> 2) * 64 + (kk & 3) * 8, v_lo + kk * (16 * 128 >> 4),
+          mma_ts(tmem + Ge::kColO + s * D, tmem + s * 128 + kk * 8, v_lo + kk * (16 * 128 >> 4),
                  kIdO, !first_tile || kk > 0);
       };
       auto wait_p = [&](int s, int u) {
@@ -402,12 +408,13 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
     }
     __syncwarp();
   } else if (warp > kMma && !FP4) {
-    // ------------------------------------------------ TMA producer: a lane a box
+    // ------------------------------------------------ TMA producers, one warp for K and one for V: a lane a box
+    const int kv = warp - kMma - 1;
     const int boxes = kTK / a.c.page;  // boxes of 64 dims a tile: boxes * D / 64 <= 16
     const int b = lane % boxes, half = lane / boxes;
-    int issued = 0, k_tile = -1;
+    int last = -1;
     uint32_t cleaned = 0;
-    // a lane's page of key tiles k_tile .. k_tile - 2 and, looked up ahead, k_tile + 1
+    // a lane's page of a key tile
     auto lookup = [&](int t) -> int {
       if (t >= nt) return -1;
       const int slot = slot0(t) + b * a.c.page;
@@ -416,23 +423,14 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
       if (pg < 0) flag_status(err, DFLASH_STATUS_BAD_PAGE);
       return pg;
     };
-    int pgs[4] = {lookup(0), -1, -1, -1};
-    for (int e = 0; e < entries; ++e) {
-      const int sl = e % kSlots;
+    int pg = lookup(0);
+    for (int t = 0; t < nt; ++t) {
+      const int e = entry_of(kv, t), sl = e % kSlots;
+      const int next = lookup(t + 1);
       bool ok = e < kSlots || mbar_wait(&empty[sl], ((e / kSlots) & 1) ^ 1u, err, DFLASH_STATUS_TIMEOUT, abort_word);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      int kv, t;
-      entry(e, &kv, &t);
       const int kb = slot0(t);
-      if (!kv) {
-        k_tile = t;
-        pgs[3] = pgs[2];
-        pgs[2] = pgs[1];
-        pgs[1] = pgs[0];
-        pgs[0] = lookup(t + 1);
-      }
-      const int pg = t == k_tile ? pgs[1] : t == k_tile - 1 ? pgs[2] : pgs[3];
       const unsigned go = __ballot_sync(0xffffffffu, pg >= 0);
       // V rows that no row sees count as zero whatever their slots hold: such a
       // tile lands on a barrier of its own and is handed on once they are
@@ -445,7 +443,7 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
       if (pg >= 0)
         tma_tile(smem_u32(tile) + half * Ge::kSub + b * a.c.page * 128, kv ? &P.vmap : &P.kmap, bar, half * 64,
                  (pg * a.c.nkv + h) * a.c.page);
-      issued = e + 1;
+      last = t;
       if (edge) {
         ok = mbar_wait(landed, cleaned, err, DFLASH_STATUS_TIMEOUT, nullptr);
         cleaned ^= 1u;
@@ -457,10 +455,16 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[sl]);
       }
+      pg = next;
     }
-    // no copy may still be landing when the slots are used again below
-    for (int e = max(0, issued - kSlots); e < issued; ++e)
-      mbar_wait(&full[e % kSlots], (e / kSlots) & 1, err, DFLASH_STATUS_TIMEOUT, nullptr);
+    // Every copy that was issued has landed when the MMAs have taken them all.
+    // After a failure give those still in flight a millisecond (a slot that has
+    // moved on since looks like one of them): the slots are used again below.
+    if (last < nt - 1 || *reinterpret_cast<volatile int*>(abort_word))
+      for (int t = max(0, last - kSlots); t <= last; ++t) {
+        const int e = entry_of(kv, t);
+        mbar_wait(&full[e % kSlots], (e / kSlots) & 1, nullptr, 0, nullptr, 2000000);
+      }
   } else if (FP4 && warp > kMma) {
     // ------------------------------------------------ 4-bit producers: a thread a key
     if constexpr (FP4) {
@@ -540,16 +544,11 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
     }
   } else {
     // ------------------------------------------------ softmax streams
-    // two warps a lane quadrant of a stream: each takes 64 keys of a tile (and
-    // half of the output's columns) of the quadrant's 32 rows, a thread a row.
-    // P lies over the warp's own scores, so the halves never wait for each
-    // other but to share a row's maximum.
-    const int s = warp >> 3, half = (warp >> 2) & 1, q4 = warp & 3;
+    // a warp a lane quadrant of a stream, a thread a row
+    const int s = warp >> 2, q4 = warp & 3;
     const int r = q4 * 32 + lane;
-    const int pair_bar = 1 + s * 4 + q4;
     const uint32_t tl = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
-    const uint32_t ts = tl + s * 128 + half * 64, to = tl + Ge::kColO + s * D + half * (D / 2);
-    float* xch = reinterpret_cast<float*>(smem + Ge::kOffXch) + s * 256;
+    const uint32_t ts = tl + s * 128, to = tl + Ge::kColO + s * D;
     const unsigned f = f0 + (PAIR ? s * kMRows : 0) + r;
     RowView rv;
     const int jr = static_cast<int>(f / a.G);
@@ -579,11 +578,10 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
         sc *= ldexpf(1.f, ex);
       }
       if (PAIR || s == 0) {
-        // this thread's half of a query row, swizzled as TMA would write it
+        // this thread's query row, swizzled as TMA would write it
         uint8_t* dst = smem + (PAIR ? s * kMRows * D * 2 : 0) + r * 128;
 #pragma unroll
-        for (int c0 = 0; c0 < D / 16; ++c0) {
-          const int c = half * (D / 16) + c0;
+        for (int c = 0; c < D / 8; ++c) {
           uint4 w = src ? reinterpret_cast<const uint4*>(src)[c] : make_uint4(0u, 0u, 0u, 0u);
           if (FP4) {
             uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -603,24 +601,21 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
     const int n_mine = PAIR ? nt : (nt + 1 - s) / 2;
     bool ok = true;
     for (int u = 0; u < n_mine; ++u) {
-      // (the two warps of a quadrant meet at a named barrier below: a wait that
-      // gives up in one of them must not leave the other there, so after a
-      // failure both go on to the barrier and stop behind it)
-      if (ok) ok = mbar_wait(&s_full[s], u & 1, err, DFLASH_STATUS_TIMEOUT, abort_word);
+      ok = mbar_wait(&s_full[s], u & 1, err, DFLASH_STATUS_TIMEOUT, abort_word);
       ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
       if (idle) {
-        if (!ok) break;
         if (lane == 0) mbar_arrive(&p_full[s]);
         continue;
       }
       tc_fence_after();
       const int kb = slot0(PAIR ? u : 2 * u + s);
       const bool whole = kb + kTK <= all_end && (kb >= lo_max || kb + kTK <= sinks);
-      uint32_t vis[2];
+      uint32_t vis[4];
       if (!whole) {
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const int base = kb + half * 64 + 32 * w;
+        for (int w = 0; w < 4; ++w) {
+          const int base = kb + 32 * w;
           uint32_t b;
           if (plain) {
             const int end = a.mode == DFLASH_MASK_CAUSAL ? q.C + rv.j + 1 : q.C + q.n;
@@ -648,40 +643,44 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
           vis[w] = rv.j >= 0 ? b : 0u;
         }
       }
-      // the row's largest score of the tile
-      float sv[64];
-      auto load_scores = [&](int c) {
-        tmem_ld32(ts + c * 32, reinterpret_cast<uint32_t*>(sv) + c * 32);
-      };
-      auto hide = [&](int c) {
+      // the row's largest score of the tile: kHold of its four chunks of 32
+      // scores stay in registers, the others are read again below
+      constexpr int kHold = Ge::kHold;
+      float sv[kHold * 32];
+      auto load_scores = [&](int c, float* x) { tmem_ld32(ts + c * 32, reinterpret_cast<uint32_t*>(x)); };
+      auto hide = [&](int c, float* x) {
         if (!whole) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (!((vis[c] >> i) & 1u)) sv[c * 32 + i] = -INFINITY;
+            if (!((vis[c] >> i) & 1u)) x[i] = -INFINITY;
         }
       };
-      load_scores(0);
-      load_scores(1);
-      tmem_wait_ld();
-      hide(0);
-      hide(1);
-      float t0 = sv[0], t1 = sv[1], t2 = sv[2], t3 = sv[3];
+      float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
+      auto most = [&](const float* x) {
 #pragma unroll
-      for (int i = 4; i < 60; i += 8) {
-        t0 = max3(t0, sv[i], sv[i + 1]);
-        t1 = max3(t1, sv[i + 2], sv[i + 3]);
-        t2 = max3(t2, sv[i + 4], sv[i + 5]);
-        t3 = max3(t3, sv[i + 6], sv[i + 7]);
+        for (int i = 0; i < 32; i += 8) {
+          t0 = max3(t0, x[i], x[i + 1]);
+          t1 = max3(t1, x[i + 2], x[i + 3]);
+          t2 = max3(t2, x[i + 4], x[i + 5]);
+          t3 = max3(t3, x[i + 6], x[i + 7]);
+        }
+      };
+#pragma unroll
+      for (int c = kHold; c < 4; ++c) {
+        load_scores(c, sv);
+        tmem_wait_ld();
+        hide(c, sv);
+        most(sv);
       }
-      float top = max3(max3(t0, sv[60], sv[61]), max3(t1, sv[62], sv[63]), fmaxf(t2, t3));
-      // the other half's maximum; its last value has been read before its scores
-      // of this tile could be issued
-      xch[half * 128 + r] = top;
-      if (named_bar_or(pair_bar, 64, ok ? 0 : 1)) {
-        ok = false;
-        break;
+#pragma unroll
+      for (int c = 0; c < kHold; ++c) load_scores(c, sv + c * 32);
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < kHold; ++c) {
+        hide(c, sv + c * 32);
+        most(sv + c * 32);
       }
-      top = fmaxf(top, xch[(half ^ 1) * 128 + r]) * sc;
+      const float top = max3(max3(t0, t1, t2), t3, t3) * sc;
       // The scores are complete, so every output product before them is too:
       // the output may be rescaled in place.
       const bool need = top > m + kRescale;
@@ -690,7 +689,7 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
         l *= alpha;
         if (u > 0) {
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
+          for (int c = 0; c < D / 16; ++c) {
             float v[16];
             tmem_ld16(to + c * 16, v);
 #pragma unroll
@@ -704,19 +703,26 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
       const uint64_t sc2 = two(sc, sc), neg2 = two(neg, neg);
       uint64_t sum0 = 0ull, sum1 = 0ull;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t pk[16];
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pk[16];  // P's columns 16c ..: over scores that have been read
+        float* x = sv + (c % kHold) * 32;
+        if (c >= kHold && c % kHold == 0) {
+#pragma unroll
+          for (int e = 0; e < kHold; ++e) load_scores(c + e, sv + e * 32);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < kHold; ++e) hide(c + e, sv + e * 32);
+        }
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
-          float* x = sv + c * 32 + i;
-          untwo(fma2(two(x[0], x[1]), sc2, neg2), x[0], x[1]);
-          untwo(fma2(two(x[2], x[3]), sc2, neg2), x[2], x[3]);
+          untwo(fma2(two(x[i], x[i + 1]), sc2, neg2), x[i], x[i + 1]);
+          untwo(fma2(two(x[i + 2], x[i + 3]), sc2, neg2), x[i + 2], x[i + 3]);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = ex2f(x[k]);
-          sum0 = add2(sum0, two(x[0], x[1]));
-          sum1 = add2(sum1, two(x[2], x[3]));
-          pk[i / 2] = pack2<FP4>(x[0], x[1]);
-          pk[i / 2 + 1] = pack2<FP4>(x[2], x[3]);
+          for (int k = 0; k < 4; ++k) x[i + k] = ex2f(x[i + k]);
+          sum0 = add2(sum0, two(x[i], x[i + 1]));
+          sum1 = add2(sum1, two(x[i + 2], x[i + 3]));
+          pk[i / 2] = pack2<FP4>(x[i], x[i + 1]);
+          pk[i / 2 + 1] = pack2<FP4>(x[i + 2], x[i + 3]);
         }
         tmem_st16(ts + c * 16, pk);
       }
@@ -735,32 +741,26 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
       tc_fence_after();
     }
     const bool mine = ok && n_mine > 0 && !idle;
-    // a row's sum is its halves' sums
-    xch[half * 128 + r] = mine ? l : 0.f;
-    named_bar_sync(pair_bar, 64);
-    l = xch[r] + xch[128 + r];
     float* xo = reinterpret_cast<float*>(smem + Ge::kOffSlots);  // [128][kPartLd] the second stream's rows
     float* xm = xo + kMRows * Ge::kPartLd;                       // [128][2]
     float m1 = -INFINITY, l1 = 0.f;
     if (!PAIR) {
       if (s == 1) {
-        if (half == 0) {
-          xm[2 * r] = mine ? m : -INFINITY;
-          xm[2 * r + 1] = mine ? l : 0.f;
-        }
+        xm[2 * r] = mine ? m : -INFINITY;
+        xm[2 * r + 1] = mine ? l : 0.f;
         if (mine) {
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
+          for (int c = 0; c < D / 16; ++c) {
             float v[16];
             tmem_ld16(to + c * 16, v);
 #pragma unroll
             for (int i = 0; i < 16; i += 4)
-              *reinterpret_cast<float4*>(xo + r * Ge::kPartLd + half * (D / 2) + c * 16 + i) =
+              *reinterpret_cast<float4*>(xo + r * Ge::kPartLd + c * 16 + i) =
                   make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
           }
         }
       }
-      named_bar_sync(9, kSoftThreads);
+      named_bar_sync(1, kSoftThreads);
       if (s == 0) {
         m1 = xm[2 * r];
         l1 = xm[2 * r + 1];
@@ -774,9 +774,9 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
       const float inv = split ? 1.f : M == -INFINITY ? 0.f : 1.f / den;
       const bool write = rv.j >= 0;
       const int64_t prow = part_row + (PAIR ? s * kMRows : 0) + r;
-      __nv_bfloat16* dst = a.out + static_cast<int64_t>(q.row0 + jr) * a.out_ld + (h * a.G + hd) * D + half * (D / 2);
+      __nv_bfloat16* dst = a.out + static_cast<int64_t>(q.row0 + jr) * a.out_ld + (h * a.G + hd) * D;
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = 0; c < D / 16; ++c) {
         float v[16];
         if (mine) {
           tmem_ld16(to + c * 16, v);
@@ -789,7 +789,7 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
         if (!PAIR && w1 > 0.f) {
 #pragma unroll
           for (int i = 0; i < 16; i += 4) {
-            const float4 x = *reinterpret_cast<const float4*>(xo + r * Ge::kPartLd + half * (D / 2) + c * 16 + i);
+            const float4 x = *reinterpret_cast<const float4*>(xo + r * Ge::kPartLd + c * 16 + i);
             v[i] = fmaf(x.x, w1, v[i]);
             v[i + 1] = fmaf(x.y, w1, v[i + 1]);
             v[i + 2] = fmaf(x.z, w1, v[i + 2]);
@@ -800,7 +800,7 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
         if (split) {
 #pragma unroll
           for (int i = 0; i < 16; i += 4)
-            *reinterpret_cast<float4*>(a.part_o + prow * D + half * (D / 2) + c * 16 + i) =
+            *reinterpret_cast<float4*>(a.part_o + prow * D + c * 16 + i) =
                 make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         } else {
 #pragma unroll
@@ -810,7 +810,7 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
                            pack2<false>(v[i + 4] * inv, v[i + 5] * inv), pack2<false>(v[i + 6] * inv, v[i + 7] * inv));
         }
       }
-      if (split && write && half == 0) *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(M, den);
+      if (split && write) *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(M, den);
     }
   }
   tc_fence_before();
