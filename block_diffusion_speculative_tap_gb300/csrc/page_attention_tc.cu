@@ -218,7 +218,7 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
   }
   const PageAttnArgs& a = P.a;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Ge::kOffBar);  // [kSlots] a tile is in its slot
-  uint64_t* empty = full + kSlots;   // [kSlots] the MMAs that read the slot are done
+  uint64_t* empty = full + kSlots;   // [kSlots] the MMAs that read the slot are done (a softmax thread says so)
   uint64_t* s_full = empty + kSlots; // [2] a stream's scores are in tensor memory
   uint64_t* p_full = s_full + 2;     // [2] its weights are, and its output is rescaled
   uint64_t* q_full = p_full + 2;     // the queries are in shared memory
@@ -357,7 +357,6 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
           if (ok) {
             scores(0, sl);
             scores(1, sl);
-            umma_commit(&empty[sl]);
           }
         }
 #pragma unroll 1
@@ -372,10 +371,8 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
             wait_p(s, t);
             if (!ok) break;
             output(s, vs, t == 0);
-            if (s == 1) umma_commit(&empty[vs]);
             if (more) scores(s, ks);
           }
-          if (ok && more) umma_commit(&empty[ks]);
         }
       } else {
 #pragma unroll 1
@@ -383,7 +380,6 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
           const int sl = wait_entry();
           if (!ok) break;
           scores(t, sl);
-          umma_commit(&empty[sl]);
         }
 #pragma unroll 1
         for (int t = 0; t < nt && ok; ++t) {
@@ -391,12 +387,10 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
           if (ok) wait_p(s, t >> 1);
           if (!ok) break;
           output(s, vs, t < 2);
-          umma_commit(&empty[vs]);
           if (t + 2 < nt) {
             const int ks = wait_entry();
             if (!ok) break;
             scores(s, ks);
-            umma_commit(&empty[ks]);
           }
         }
       }
@@ -604,6 +598,14 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
       ok = mbar_wait(&s_full[s], u & 1, err, DFLASH_STATUS_TIMEOUT, abort_word);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
+      // These scores are complete, and so is every MMA issued before them: the
+      // slot of their K is free, and that of the V before. (Said here: a commit
+      // of its own would cost the issuing thread the time of one and a half MMAs.)
+      if (q4 == 0 && lane == 0 && (!PAIR || s == 1)) {
+        const int t = PAIR ? u : 2 * u + s, tv = PAIR ? t - 1 : t - 2;
+        mbar_arrive(&empty[entry_of(0, t) % kSlots]);
+        if (tv >= 0) mbar_arrive(&empty[entry_of(1, tv) % kSlots]);
+      }
       if (idle) {
         if (lane == 0) mbar_arrive(&p_full[s]);
         continue;
