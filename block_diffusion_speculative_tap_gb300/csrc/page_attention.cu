@@ -148,7 +148,10 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
   for (bool first = true;; first = false) {
   if (warp == 0) run_next(a, &run, first);
   __syncthreads();
-  if (!run.left) return;
+  if (!run.left) {
+    if (first && threadIdx.x == 0) write_join(a, run);
+    return;
+  }
   const Segment& sg = run.seg;
   const StreamRows q = sg.q;
   const int h = sg.h, lo = sg.lo, lo_max = sg.lo_max, hi = sg.hi, sinks = sg.sinks, i0 = sg.i0, i1 = sg.i1;
@@ -216,6 +219,8 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
   for (int s = 0; s < kST; ++s) fetch_pages(i0 + warp + s * kWarps, pg[s]);
 #pragma unroll
   for (int s = 0; s < kST - 1; ++s) issue(i0 + warp + s * kWarps, s, pg[s]);
+
+  if (first && threadIdx.x == 0) write_join(a, run);
 
   // this lane's rows 8b + 2t, 8b + 2t + 1 of the scores
   RowView rv[NB][2];
@@ -597,62 +602,33 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
   }
 }
 
-// Joins the parts of the tiles that a boundary between two CTAs' shares cuts:
-// a CTA a boundary and rows of its tile, a warp a row.
+// Joins the parts of the tiles that the boundaries between CTAs' shares cut: a
+// CTA a boundary (and rows of its tile).
+//
+// Tiles of up to 16 rows: a warp a row, kAhead parts loaded before any is used
+// (a token of 8 kv heads over all SMs is 19 parts of few rows: 15.4 -> 12.8 us
+// a call).
 constexpr int kCombineRows = 8;
-// kAhead: parts whose rows are loaded before any is used. A token of 8 kv heads
-// over all SMs is 19 parts of few rows (20 ahead: 15.4 -> 12.8 us a call); the
-// large tiles have two or three parts of many rows, where the registers would
-// cost residence (blocks 77 -> 103 us with 20).
-template <int D, int kAhead>
+constexpr int kAhead = 20;
+template <int D>
 __global__ void __launch_bounds__(kCombineRows * 32) page_combine_kernel(const __grid_constant__ PageAttnArgs a) {
   constexpr int kE = D / 32;
-  __shared__ Segment seg_s;
-  __shared__ int slot_s, parts_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // row_start and lens were complete before the attention kernel let this one start
-  if (warp == 0) {
-    int parts = 0, slot = 0;
-    LaneStream x;
-    const Share sh = share_of(a, x);
-    const int b = static_cast<int>(blockIdx.x) + 1;
-    Segment sg{};
-    if (!sh.whole && b < sh.ctas) {
-      const int at = sh.start(b);
-      if (segment_at(a, sh, at, 1, a.r.S <= 32, x, &sg)) {
-        const int from = at - sg.x0, to = from + sg.u, before = sh.start(b - 1);
-        if (sg.x0 > 0 && before <= from) {  // the first boundary inside the tile
-          slot = 2 * (b - 1) + (before == from ? 0 : 1);
-          // the CTAs whose share starts before the tile's end: total * k / ctas < to, so k < to * ctas / total
-          const long long total = static_cast<long long>(sh.line) * a.c.nkv;
-          parts = static_cast<int>((static_cast<long long>(to) * sh.ctas + total - 1) / total) - (b - 1);
-        }
-      }
-    }
-    if (lane == 0) {
-      seg_s = sg;
-      slot_s = slot;
-      parts_s = parts;
-    }
-  }
   pdl_wait();
   pdl_trigger();
-  __syncthreads();
-  const int parts = parts_s;
-  if (parts == 0) return;
-  const Segment& sg = seg_s;
-  const StreamRows q = sg.q;
+  const int b = static_cast<int>(blockIdx.x) + 1;
+  const JoinRecord jr = a.join[b];
+  if (jr.parts == 0) return;
   const int r = blockIdx.y * kCombineRows + warp;
-  const unsigned f = static_cast<unsigned>(sg.tile * a.tile + r);
+  const unsigned f = jr.f0 + r;
   const int j = static_cast<int>(f / a.G);
-  if (r >= a.tile || j >= q.n) return;
-  const int next = 2 * (static_cast<int>(blockIdx.x) + 1);  // slot of the second part; the others follow by 2
-  auto row_of = [&](int k) { return static_cast<int64_t>(k == 0 ? slot_s : next + 2 * (k - 1)) * a.tile + r; };
+  if (r >= a.tile || j >= jr.n) return;
+  auto row_of = [&](int k) { return static_cast<int64_t>(k == 0 ? jr.slot : 2 * (b + k - 1)) * a.tile + r; };
   float M = -INFINITY, den = 0.f;
   float acc[kE] = {};
   // 32 parts at a time: a lane a part's (maximum, sum), all parts' rows in flight
-  for (int k0 = 0; k0 < parts; k0 += 32) {
-    const int n = min(32, parts - k0);
+  for (int k0 = 0; k0 < jr.parts; k0 += 32) {
+    const int n = min(32, jr.parts - k0);
     float2 ml = make_float2(-INFINITY, 0.f);
     if (lane < n) ml = *reinterpret_cast<const float2*>(a.part_ml + row_of(k0 + lane) * 2);
     float mx = ml.x;
@@ -694,7 +670,7 @@ __global__ void __launch_bounds__(kCombineRows * 32) page_combine_kernel(const _
   }
   const float inv = M == -INFINITY ? 0.f : 1.f / den;
   const int hd = static_cast<int>(f - j * a.G);
-  __nv_bfloat16* dst = a.out + static_cast<int64_t>(q.row0 + j) * a.out_ld + (sg.h * a.G + hd) * D + lane * kE;
+  __nv_bfloat16* dst = a.out + static_cast<int64_t>(jr.row0 + j) * a.out_ld + (jr.h * a.G + hd) * D + lane * kE;
   if (kE == 4) {
     uint2 w;
     w.x = pack2(acc[0] * inv, acc[1 % kE] * inv, false);
@@ -705,6 +681,46 @@ __global__ void __launch_bounds__(kCombineRows * 32) page_combine_kernel(const _
   } else {
     *dst = __float2bfloat16_rn(acc[0] * inv);
   }
+}
+
+// Tiles of 128 rows and more, whose parts lie by columns of four dims: a lane a
+// row, a warp eight of the row's dims.
+constexpr int kCombineTile = 32;
+template <int D>
+__global__ void __launch_bounds__(D * 4) page_combine_tile_kernel(const __grid_constant__ PageAttnArgs a) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_trigger();
+  const int b = static_cast<int>(blockIdx.x) + 1;
+  const JoinRecord jr = a.join[b];
+  if (jr.parts == 0) return;
+  const int r = blockIdx.y * kCombineTile + lane;
+  const unsigned f = jr.f0 + r;
+  const int j = static_cast<int>(f / a.G);
+  if (j >= jr.n) return;
+  auto slot_of = [&](int k) { return static_cast<int64_t>(k == 0 ? jr.slot : 2 * (b + k - 1)) * a.tile; };
+  float M = -INFINITY, den = 0.f;
+  float acc[8] = {};
+#pragma unroll 3
+  for (int k = 0; k < jr.parts; ++k) {
+    const int64_t s = slot_of(k);
+    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (s + r) * 2);
+    const float4 x = *reinterpret_cast<const float4*>(a.part_o + s * D + (2 * warp * a.tile + r) * 4);
+    const float4 y = *reinterpret_cast<const float4*>(a.part_o + s * D + ((2 * warp + 1) * a.tile + r) * 4);
+    const float top = fmaxf(M, ml.x);
+    if (top == -INFINITY) continue;
+    const float old = ex2f(M - top), w = ex2f(ml.x - top);
+    M = top;
+    den = fmaf(den, old, w * ml.y);
+    const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = fmaf(acc[e], old, w * v[e]);
+  }
+  const float inv = M == -INFINITY ? 0.f : 1.f / den;
+  const int hd = static_cast<int>(f - j * a.G);
+  *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(jr.row0 + j) * a.out_ld + (jr.h * a.G + hd) * D + warp * 8) =
+      make_uint4(pack2(acc[0] * inv, acc[1] * inv, false), pack2(acc[2] * inv, acc[3] * inv, false),
+                 pack2(acc[4] * inv, acc[5] * inv, false), pack2(acc[6] * inv, acc[7] * inv, false));
 }
 
 // A kernel's shared-memory limit, raised once a device.
@@ -732,10 +748,14 @@ int launch_small_any(const PageAttnArgs& a, const PagePlan& p, bool fp4, cudaStr
 
 template <int D>
 int launch_combine(const PageAttnArgs& a, const PagePlan& p, cudaStream_t st) {
-  const cudaError_t e = launch_pdl(a.tile > 16 ? page_combine_kernel<D, 3> : page_combine_kernel<D, 20>,
-                                   dim3(static_cast<unsigned>(p.target - 1),
-                                        static_cast<unsigned>((a.tile + kCombineRows - 1) / kCombineRows)),
-                                   dim3(kCombineRows * 32), 0, st, a);
+  const unsigned cuts = static_cast<unsigned>(p.target - 1);
+  cudaError_t e;
+  if (a.tile > 16)
+    e = launch_pdl(page_combine_tile_kernel<D>, dim3(cuts, static_cast<unsigned>(a.tile / kCombineTile)), dim3(D * 4), 0,
+                   st, a);
+  else
+    e = launch_pdl(page_combine_kernel<D>, dim3(cuts, static_cast<unsigned>((a.tile + kCombineRows - 1) / kCombineRows)),
+                   dim3(kCombineRows * 32), 0, st, a);
   count_launch();
   return cuda_status(e);
 }

@@ -58,7 +58,7 @@ struct TcGeo {
   static constexpr int kOffRaw = kOffSlots + kSlots * kSlot;
   static constexpr int kOffBar = kOffRaw + kStage * kRaw;
   static constexpr int kSmem = kOffBar + 512;
-  static constexpr int kHold = FP4 ? 2 : 4;  // of a tile's four chunks of 32 scores, those kept in registers
+  static constexpr int kHold = FP4 ? 1 : 2;  // of a tile's four chunks of 32 scores, those kept in registers
   static constexpr int kPartLd = D + 4;
   static constexpr int kColO = 256;
   static constexpr float kShift = FP4 ? 7.f : 0.f;  // P <= 2^(kRescale + kShift) in fp16
@@ -258,6 +258,7 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (first && threadIdx.x == 32 * kMma) write_join(a, *run);
   if (!run->left) break;
   const uint32_t tmem = *tmem_slot;
   const Segment& it = run->seg;
@@ -556,17 +557,26 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
       const __nv_bfloat16* src =
           rv.j >= 0 ? a.q + static_cast<int64_t>(q.row0 + jr) * a.q_ld + (h * a.G + hd) * D : nullptr;
       float down = 1.f;
+      uint4 w[8];  // 64 dims in flight at a time
+      auto fetch = [&](int c0) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          w[c] = src ? reinterpret_cast<const uint4*>(src)[c0 + c] : make_uint4(0u, 0u, 0u, 0u);
+      };
       if (FP4) {
         // into fp16 over a power of two a row
         float top = 0.f;
-        if (src)
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 w = reinterpret_cast<const uint4*>(src)[c];
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int c0 = 0; c0 < D / 8; c0 += 8) {
+          fetch(c0);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-              top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[x] << 16)), fabsf(__uint_as_float(u[x] & 0xffff0000u))));
+              top = max3(top, fabsf(__uint_as_float(u[x] << 16)), fabsf(__uint_as_float(u[x] & 0xffff0000u)));
           }
+        }
         const int ex = (top > 0.f && top < INFINITY) ? max(-100, min(126, ilogbf(top))) : 0;
         down = ldexpf(1.f, -ex);
         sc *= ldexpf(1.f, ex);
@@ -575,16 +585,19 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
         // this thread's query row, swizzled as TMA would write it
         uint8_t* dst = smem + (PAIR ? s * kMRows * D * 2 : 0) + r * 128;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          uint4 w = src ? reinterpret_cast<const uint4*>(src)[c] : make_uint4(0u, 0u, 0u, 0u);
-          if (FP4) {
-            uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        for (int c0 = 0; c0 < D / 8; c0 += 8) {
+          fetch(c0);
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              u[x] = pack2<true>(__uint_as_float(u[x] << 16) * down, __uint_as_float(u[x] & 0xffff0000u) * down);
-            w = make_uint4(u[0], u[1], u[2], u[3]);
+          for (int c = 0; c < 8; ++c) {
+            if (FP4) {
+              uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                u[x] = pack2<true>(__uint_as_float(u[x] << 16) * down, __uint_as_float(u[x] & 0xffff0000u) * down);
+              w[c] = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+            *reinterpret_cast<uint4*>(dst + (c0 >> 3) * Ge::kSub + ((c ^ (r & 7)) << 4)) = w[c];
           }
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * Ge::kSub + (((c & 7) ^ (r & 7)) << 4)) = w;
         }
         fence_async();
         __syncwarp();
@@ -710,10 +723,10 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
         float* x = sv + (c % kHold) * 32;
         if (c >= kHold && c % kHold == 0) {
 #pragma unroll
-          for (int e = 0; e < kHold; ++e) load_scores(c + e, sv + e * 32);
+          for (int e = 0; e < kHold && c + e < 4; ++e) load_scores(c + e, sv + e * 32);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < kHold; ++e) hide(c + e, sv + e * 32);
+          for (int e = 0; e < kHold && c + e < 4; ++e) hide(c + e, sv + e * 32);
         }
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
@@ -775,7 +788,7 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
       const float den = (w0 > 0.f ? w0 * l : 0.f) + (w1 > 0.f ? w1 * l1 : 0.f);
       const float inv = split ? 1.f : M == -INFINITY ? 0.f : 1.f / den;
       const bool write = rv.j >= 0;
-      const int64_t prow = part_row + (PAIR ? s * kMRows : 0) + r;
+      const int trow = (PAIR ? s * kMRows : 0) + r;  // parts lie by columns of four dims: a warp's rows side by side
       __nv_bfloat16* dst = a.out + static_cast<int64_t>(q.row0 + jr) * a.out_ld + (h * a.G + hd) * D;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
@@ -802,7 +815,7 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
         if (split) {
 #pragma unroll
           for (int i = 0; i < 16; i += 4)
-            *reinterpret_cast<float4*>(a.part_o + prow * D + c * 16 + i) =
+            *reinterpret_cast<float4*>(a.part_o + part_row * D + ((c * 16 + i) / 4 * a.tile + trow) * 4) =
                 make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         } else {
 #pragma unroll
@@ -812,7 +825,7 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
                            pack2<false>(v[i + 4] * inv, v[i + 5] * inv), pack2<false>(v[i + 6] * inv, v[i + 7] * inv));
         }
       }
-      if (split && write) *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(M, den);
+      if (split && write) *reinterpret_cast<float2*>(a.part_ml + (part_row + trow) * 2) = make_float2(M, den);
     }
   }
   tc_fence_before();

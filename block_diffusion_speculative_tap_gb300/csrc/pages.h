@@ -27,6 +27,15 @@ struct RowsArgs {
   int* status;           // device status word, may be null
 };
 
+// What page_combine_kernel has to know of the tile that the boundary before
+// CTA b's share cuts first, written by that CTA.
+struct JoinRecord {
+  int parts;           // 0: no such tile
+  int slot;            // slot of the first part; the others are 2b, 2b + 2, ..
+  int h, row0, n;      // kv head, first row and rows of the stream
+  unsigned f0;         // the tile's first (row, head) pair
+};
+
 struct PageAttnArgs {
   PagesArgs c;
   RowsArgs r;
@@ -43,8 +52,9 @@ struct PageAttnArgs {
   int target;            // CTAs of one wave
   int min_units;         // fewest units a CTA's share has
   int no_split;          // tiles of up to this many units are not split
-  float* part_o;         // [2 * target][tile][d]; null: nothing is split
+  float* part_o;         // [2 * target][tile][d] (tiles of 128 rows and more: [d / 4][tile][4]); null: nothing is split
   float* part_ml;        // [2 * target][tile][2]
+  JoinRecord* join;      // [target]
 };
 
 __device__ __forceinline__ void flag_status(int* status, int bits) {
@@ -275,6 +285,29 @@ __device__ __forceinline__ void run_next(const PageAttnArgs& a, Run* run, bool b
       run->at = at + (sh.whole ? 1 : g.x1 - g.x0);
     }
   }
+}
+
+// The CTA's record, from its first segment. One lane.
+__device__ __forceinline__ void write_join(const PageAttnArgs& a, const Run& run) {
+  const int b = static_cast<int>(blockIdx.x);
+  if (a.part_o == nullptr || b >= a.target) return;
+  JoinRecord j{0, 0, 0, 0, 0, 0};
+  const Segment& g = run.seg;
+  if (run.left && g.x0 > 0) {  // the share starts inside a tile (never a CTA's first, nor with whole tiles)
+    const Share& sh = run.sh;
+    const int at = sh.start(b), from = at - g.x0, to = from + g.u, before = sh.start(b - 1);
+    if (before <= from) {  // the first boundary inside it
+      j.slot = 2 * (b - 1) + (before == from ? 0 : 1);
+      // the CTAs whose share starts before the tile's end: total * k / ctas < to, so k < to * ctas / total
+      const long long total = static_cast<long long>(sh.line) * a.c.nkv;
+      j.parts = static_cast<int>((static_cast<long long>(to) * sh.ctas + total - 1) / total) - (b - 1);
+      j.h = g.h;
+      j.row0 = g.q.row0;
+      j.n = g.q.n;
+      j.f0 = static_cast<unsigned>(g.tile) << a.tile_log2;
+    }
+  }
+  a.join[b] = j;
 }
 
 // What one (query row, head) pair of a tile sees.

@@ -78,7 +78,9 @@ bool good_rows(const void* p, int64_t ld, int64_t heads, int d) {
 }
 
 size_t attention_ws(const PagePlan& p, const dflash_pages& c) {
-  return p.split ? static_cast<size_t>(2 * p.target) * p.tile * (c.head_dim + 2) * sizeof(float) : 0;
+  return p.split ? static_cast<size_t>(2 * p.target) * p.tile * (c.head_dim + 2) * sizeof(float) +
+                       static_cast<size_t>(p.target) * sizeof(JoinRecord)
+                 : 0;
 }
 
 int check_heads(const dflash_pages* c, const dflash_rows* r, int nq) {
@@ -193,6 +195,7 @@ int dflash_page_attention(const dflash_pages* c, const dflash_rows* r, int n_q_h
   a.no_split = p.no_split;
   a.part_o = p.split ? static_cast<float*>(ws) : nullptr;
   a.part_ml = p.split ? a.part_o + static_cast<size_t>(2 * p.target) * p.tile * c->head_dim : nullptr;
+  a.join = p.split ? reinterpret_cast<JoinRecord*>(a.part_ml + static_cast<size_t>(2 * p.target) * p.tile * 2) : nullptr;
   return launch_page_attention(a, p, c->format == DFLASH_PAGES_FP4, reinterpret_cast<cudaStream_t>(stream));
 }
 
