@@ -5,7 +5,7 @@
 //   out_r = sum_c softmax_c(scale * q_r . k_c) v_c  over the slots c row r sees
 //
 // in one pass over the keys: a running maximum m (log2 domain), sum l and
-// output O in fp32, rescaled when the maximum moves. The products are taken
+// output O in fp32, rescaled when the maximum has moved by more than 2^8. The products are taken
 // transposed, S^T = K Q^T and O^T = V^T P^T, on m16n8k16 MMAs: 16 keys (16
 // dims) on M and one or two blocks of 8 rows on N, so a token of up to 8 heads
 // a kv head wastes no rows and the heads share every K/V byte.
@@ -38,6 +38,7 @@ namespace dfl {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr float kRescale = 8.f;  // log2 by which the maximum in use may lag
 
 template <int D, bool FP4, int NB>
 struct Geo {
@@ -55,7 +56,7 @@ struct Geo {
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kMerge = kWarps * kTile * (kPartLd + 2) * 4;
   static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
-  static constexpr float kShift = FP4 ? 8.f : 0.f;  // log2 of the factor P carries into fp16
+  static constexpr float kShift = FP4 ? 7.f : 0.f;  // P <= 2^(kRescale + kShift) in fp16
 };
 
 // 16-byte piece of a row at which piece p of key `key` is kept, so that the
@@ -394,26 +395,27 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
     uint32_t pb[NB][kSub][2];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      float mx[2] = {-INFINITY, -INFINITY};
+      float mx[2] = {-INFINITY, -INFINITY}, sub[2];
 #pragma unroll
       for (int kt = 0; kt < kSub; ++kt) {
         mx[0] = fmaxf(mx[0], fmaxf(s[b][kt][0], s[b][kt][2]));
         mx[1] = fmaxf(mx[1], fmaxf(s[b][kt][1], s[b][kt][3]));
       }
-      bool moved = false;
-      float al[2], sub[2];
+      // the maximum in use moves when a score passes it by 2^kRescale: rarely
+      // after a row's first units, and until then no lane asks the others
+      const bool need = mx[0] * sc[b][0] > m[b][0] + kRescale || mx[1] * sc[b][1] > m[b][1] + kRescale;
+      if (__any_sync(0xffffffffu, need)) {
+        float al[2];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 4));
-        mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 8));
-        mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 16));
-        const float mn = fmaxf(m[b][x], mx[x] * sc[b][x]);
-        al[x] = m[b][x] == mn ? 1.f : ex2f(m[b][x] - mn);
-        moved |= m[b][x] != mn;
-        m[b][x] = mn;
-        sub[x] = mn == -INFINITY ? 0.f : mn - G_::kShift;
-      }
-      if (__any_sync(0xffffffffu, moved)) {
+        for (int x = 0; x < 2; ++x) {
+          mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 4));
+          mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 8));
+          mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 16));
+          const float mn = fmaxf(m[b][x], mx[x] * sc[b][x]);
+          al[x] = m[b][x] == mn ? 1.f : ex2f(m[b][x] - mn);
+          m[b][x] = mn;
+          l[b][x] *= al[x];
+        }
 #pragma unroll
         for (int e = 0; e < kMT; ++e) {
           o[b][e][0] *= al[0];
@@ -421,9 +423,9 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
           o[b][e][2] *= al[0];
           o[b][e][3] *= al[1];
         }
-        l[b][0] *= al[0];
-        l[b][1] *= al[1];
       }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) sub[x] = m[b][x] == -INFINITY ? 0.f : m[b][x] - G_::kShift;
 #pragma unroll
       for (int kt = 0; kt < kSub; ++kt) {
         float* x = s[b][kt];
@@ -509,16 +511,21 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
         }
 #pragma unroll
         for (int x = 0; x < kVW; ++x) {
+          // the codes of two keys are paired before they are converted: byte e
+          // of f[2i] holds dim 2e of both, of f[2i + 1] dim 2e + 1
+          constexpr uint32_t kLow = 0x0f0f0f0fu;
           uint32_t f[4][4];
 #pragma unroll
-          for (int k2 = 0; k2 < 4; ++k2) e2m1x8(w[k2][x], f[k2]);
+          for (int i2 = 0; i2 < 2; ++i2) {
+            const uint32_t ka = w[2 * i2][x], kc = w[2 * i2 + 1][x];
+            e2m1x8((ka & kLow) | ((kc << 4) & ~kLow), f[2 * i2]);
+            e2m1x8(((ka >> 4) & kLow) | (kc & ~kLow), f[2 * i2 + 1]);
+          }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             if (x * 4 + e >= kMT) continue;
-            const uint32_t v[4] = {hmul2(__byte_perm(f[0][e], f[1][e], 0x5410), vsc[0]),
-                                   hmul2(__byte_perm(f[0][e], f[1][e], 0x7632), vsc[0]),
-                                   hmul2(__byte_perm(f[2][e], f[3][e], 0x5410), vsc[1]),
-                                   hmul2(__byte_perm(f[2][e], f[3][e], 0x7632), vsc[1])};
+            const uint32_t v[4] = {hmul2(f[0][e], vsc[0]), hmul2(f[1][e], vsc[0]), hmul2(f[2][e], vsc[1]),
+                                   hmul2(f[3][e], vsc[1])};
 #pragma unroll
             for (int b = 0; b < NB; ++b) mma16816<FP4>(o[b][x * 4 + e], v, pb[b][kt][0], pb[b][kt][1]);
           }
