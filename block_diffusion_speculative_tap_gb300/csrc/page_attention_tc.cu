@@ -12,9 +12,9 @@
 //   parity: one 128-row tile, the streams take the even and the odd key tiles
 //           and are joined at the end (blocks and trees, where the cache's
 //           bytes are the bound).
-// One warp issues all MMAs in order: S_s(u+1) is issued behind P_s(u) V(u), so
-// the completion of scores also says that every earlier output product is
-// done, and a row's output may be rescaled then. The maximum in use moves only
+// A stream's MMAs are issued by one thread in order: S(u+1) behind P(u) V(u), so
+// the completion of scores also says that every earlier output product of the
+// stream is done, and a row's output may be rescaled then. The maximum in use moves only
 // when the true one passes it by 2^8, so rescaling is rare after a row's
 // first tiles.
 //
@@ -41,12 +41,13 @@ constexpr int kMRows = 128;              // rows of a softmax stream
 constexpr float kRescale = 8.f;          // log2 by which the maximum in use may lag
 constexpr int kSoftWarps = 8;            // two streams x four lane quadrants
 constexpr int kSoftThreads = 32 * kSoftWarps;
-constexpr int kMma = kSoftWarps;         // the MMA warp; the producers follow
+constexpr int kMma = kSoftWarps;         // two MMA warps; the producers follow
+constexpr int kProducer = kMma + 2;
 
 template <int D, bool FP4, bool PAIR>
 struct TcGeo {
   static constexpr int kProd = FP4 ? 4 : 2;                 // producer warps (bf16: K, V)
-  static constexpr int kThreads = kSoftThreads + 32 + 32 * kProd;
+  static constexpr int kThreads = kSoftThreads + 64 + 32 * kProd;
   static constexpr int kSub = kTK * 128;                    // 128 rows x 64 dims
   static constexpr int kSlot = kTK * D * 2;                 // a K or V tile
   static constexpr int kQ = (PAIR ? 2 : 1) * kMRows * D * 2;
@@ -58,7 +59,9 @@ struct TcGeo {
   static constexpr int kOffRaw = kOffSlots + kSlots * kSlot;
   static constexpr int kOffBar = kOffRaw + kStage * kRaw;
   static constexpr int kSmem = kOffBar + 512;
-  static constexpr int kHold = FP4 ? 1 : 2;  // of a tile's four chunks of 32 scores, those kept in registers
+  static constexpr int kHold = !FP4 && PAIR ? 2 : 1;  // of a tile's four chunks of 32 scores, those kept in registers
+  static constexpr int kParts = PAIR ? 1 : 2;         // P is handed on whole, or 64 keys at a time
+  static constexpr int kIssuers = PAIR ? 1 : 2;       // threads that issue MMAs
   static constexpr int kPartLd = D + 4;
   static constexpr int kColO = 256;
   static constexpr float kShift = FP4 ? 7.f : 0.f;  // P <= 2^(kRescale + kShift) in fp16
@@ -123,6 +126,21 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr)
       : "memory");
+}
+// The same, and the largest of the 32 values as fp32 (NaN never).
+__device__ __forceinline__ void tmem_ld32_max(uint32_t taddr, uint32_t* r, float& most) {
+  uint32_t m;
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(m)
+      : "r"(taddr)
+      : "memory");
+  most = __uint_as_float(m);
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -218,12 +236,12 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
   }
   const PageAttnArgs& a = P.a;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Ge::kOffBar);  // [kSlots] a tile is in its slot
-  uint64_t* empty = full + kSlots;   // [kSlots] the MMAs that read the slot are done (a softmax thread says so)
+  uint64_t* empty = full + kSlots;   // [kSlots] the MMAs that read the slot are done (a softmax thread of each reader says so)
   uint64_t* s_full = empty + kSlots; // [2] a stream's scores are in tensor memory
-  uint64_t* p_full = s_full + 2;     // [2] its weights are, and its output is rescaled
-  uint64_t* q_full = p_full + 2;     // the queries are in shared memory
-  uint64_t* o_full = q_full + 1;     // every MMA is done
-  uint64_t* landed = o_full + 1;     // a tile that has to be cleaned is in its slot
+  uint64_t* p_full = s_full + 2;     // [2][2] its weights are (of 64 keys, or all), and its output is rescaled
+  uint64_t* q_full = p_full + 4;     // the queries are in shared memory
+  uint64_t* o_full = q_full + 1;     // [2] every MMA of a stream is done
+  uint64_t* landed = o_full + 2;     // a tile that has to be cleaned is in its slot
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(landed + 1);
   int* abort_word = reinterpret_cast<int*>(tmem_slot + 1);
   Run* run = reinterpret_cast<Run*>(smem + Ge::kOffBar + 256);
@@ -243,14 +261,16 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
   if (threadIdx.x == 32) {
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&full[s], FP4 ? 32 * Ge::kProd : 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], PAIR ? 2 : 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], kSoftWarps / 2);
+      mbar_init(&p_full[2 * s], kSoftWarps / 2);
+      mbar_init(&p_full[2 * s + 1], kSoftWarps / 2);
     }
     mbar_init(q_full, PAIR ? kSoftWarps : kSoftWarps / 2);
-    mbar_init(o_full, 1);
+    mbar_init(&o_full[0], 1);
+    mbar_init(&o_full[1], 1);
     mbar_init(landed, 1);
     if (first) *abort_word = 0;
     fence_barrier_init();
@@ -284,127 +304,121 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
     const int p = col < a.c.cols ? a.c.table[static_cast<int64_t>(it.s) * a.c.cols + col] : -1;
     return p >= 0 && p < a.c.n_pages ? p : -1;
   };
-  // The ring's order: pair: K0 V0 K1 V1 ..; parity: K0 K1 V0 K2 V1 K3 ...
-  // Entry e: K (kv 0) or V (kv 1) of tile t.
+  // Rings of slots: in pair mode one for both streams, each of which takes every
+  // tile; in parity mode one a stream. A wait for a phase of a barrier only tells
+  // it from the phases next to it, so a ring has to be used in order by every
+  // thread that waits on it: no thread is ever more than one phase away.
+  // K of tile t is the ring's use 2u, its V the use 2u + 1 (u = t, or t / 2).
+  constexpr int kRing = PAIR ? kSlots : kSlots / 2;
   const int entries = 2 * nt;
+  auto use_of = [&](int kv, int t) { return 2 * (PAIR ? t : t >> 1) + kv; };
+  auto slot_of = [&](int kv, int t) { return (PAIR ? 0 : (t & 1) * kRing) + use_of(kv, t) % kRing; };
+  auto phase_of = [&](int kv, int t) { return use_of(kv, t) / kRing; };
+  // One producer's order (4-bit pages): pair K0 V0 K1 V1 ..; parity K0 K1 V0 V1 K2 K3 ..
   auto entry = [&](int e, int* kv, int* t) {
-    if (PAIR || nt < 2) {
-      *kv = e & 1;
-      *t = e >> 1;
-    } else if (e < 2) {
-      *kv = 0;
-      *t = e;
-    } else if (e == entries - 1) {
-      *kv = 1;
-      *t = nt - 1;
-    } else {
-      *kv = (e & 1) ? 0 : 1;
-      *t = (e & 1) ? (e + 1) >> 1 : (e - 2) >> 1;
-    }
+    const bool both = !PAIR && (e | 3) < entries;  // the group of four has two tiles
+    *kv = both ? (e >> 1) & 1 : e & 1;
+    *t = PAIR ? e >> 1 : 2 * (e >> 2) + (both ? e & 1 : 0);
   };
+  auto tile_of = [&](int s, int u) { return PAIR ? u : 2 * u + s; };  // a stream's key tiles
 
-  auto entry_of = [&](int kv, int t) {  // its inverse
-    if (PAIR || nt < 2) return 2 * t + kv;
-    if (kv) return t == nt - 1 ? entries - 1 : 2 * t + 2;
-    return t < 2 ? t : 2 * t - 1;
-  };
-
-  if (warp == kMma) {
-    // ------------------------------------------------ MMA issuer: one thread, and little code:
-    // whatever it does between MMAs the tensor cores stand still for
-    if (lane == 0) {
+  if (warp == kMma || warp == kMma + 1) {
+    // ------------------------------------------------ MMA issuers
+    // Issuing takes as long as the MMAs run, and a wait that is over at once
+    // still takes 100 cycles. Parity: a thread a stream, so that one waits while
+    // the other issues (blocks 62 -> 60 us, trees 130 -> 122 us). Pair: one thread
+    // for both, since there the streams' MMAs in turn would double the time until
+    // either's scores are ready (a 4096-row chunk: 367 us with one, 408 us with two).
+    if (lane == 0 && warp - kMma < Ge::kIssuers) {
       constexpr uint32_t kIdS = idesc16(FP4, kMRows, kTK, false);
       constexpr uint32_t kIdO = idesc16(FP4, kMRows, D, true);
-      const uint32_t q_lo = desc_lo(sbase, 1), slots = sbase + Ge::kOffSlots;
+      const uint32_t slots = sbase + Ge::kOffSlots;
       bool ok = nt > 0 && mbar_wait(q_full, 0, err, DFLASH_STATUS_TIMEOUT, abort_word);
-      bool any = false;
-      int slot = 0;        // next ring slot, and the parity of its phase
-      uint32_t phase = 0;
-      auto wait_entry = [&]() -> int {
-        const int sl = slot;
-        ok = mbar_wait(&full[sl], phase, err, DFLASH_STATUS_TIMEOUT, abort_word);
-        if (++slot == kSlots) {
-          slot = 0;
-          phase ^= 1u;
+      // the next use of this thread's ring
+      uint32_t ring = slots + (PAIR ? 0 : (warp - kMma) * kRing * Ge::kSlot), at = 0, parity = 0;
+      uint64_t* ring_full = full + (PAIR ? 0 : (warp - kMma) * kRing);
+      auto wait_tile = [&]() -> uint32_t {
+        ok = mbar_wait(&ring_full[at], parity, err, DFLASH_STATUS_TIMEOUT, abort_word);
+        const uint32_t tile = ring + at * Ge::kSlot;
+        if (++at == kRing) {
+          at = 0;
+          parity ^= 1u;
         }
-        return sl;
+        return tile;
       };
-      auto scores = [&](int s, int sl) {
+      // O (+)= P V of the stream's tile u, as its weights come
+      auto output = [&](int s, int u, uint32_t v) {
+        const uint32_t v_lo = desc_lo(v, Ge::kSub >> 4);
+#pragma unroll
+        for (int hf = 0; hf < Ge::kParts; ++hf) {
+          if (ok) ok = mbar_wait(&p_full[2 * s + hf], u & 1, err, DFLASH_STATUS_TIMEOUT, abort_word);
+          if (!ok) return;
+          tc_fence_after();
+#pragma unroll
+          for (int k4 = 0; k4 < kTK / 16 / Ge::kParts; ++k4) {
+            const int kk = hf * (kTK / 32) + k4;
+            mma_ts(tmem + Ge::kColO + s * D, tmem + s * 128 + kk * 8, v_lo + kk * (16 * 128 >> 4), kIdO,
+                   u > 0 || kk > 0);
+          }
+        }
+      };
+      // S = Q K^T of its next tile, behind the product that still reads P there
+      auto scores = [&](int s, uint32_t k) {
+        const uint32_t k_lo = desc_lo(k, 1), q_lo = desc_lo(sbase + (PAIR ? s * kMRows * D * 2 : 0), 1);
         tc_fence_after();
-        const uint32_t k_lo = desc_lo(slots + sl * Ge::kSlot, 1), a_lo = q_lo + (PAIR ? s * (kMRows * D * 2 >> 4) : 0);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * Ge::kSub + (kk & 3) * 32) >> 4;
-          if (kk == 0) mma_ss<false>(tmem + s * 128, a_lo, k_lo, kIdS);
-          else mma_ss<true>(tmem + s * 128, a_lo + off, k_lo + off, kIdS);
+          if (kk == 0) mma_ss<false>(tmem + s * 128, q_lo, k_lo, kIdS);
+          else mma_ss<true>(tmem + s * 128, q_lo + off, k_lo + off, kIdS);
         }
-        any = true;
         umma_commit(&s_full[s]);
       };
-      auto output = [&](int s, int sl, bool first_tile) {
-        tc_fence_after();
-        const uint32_t v_lo = desc_lo(slots + sl * Ge::kSlot, Ge::kSub >> 4);
-#pragma unroll
-        for (int kk = 0; kk < kTK / 16; ++kk)
-          mma_ts(tmem + Ge::kColO + s * D, tmem + s * 128 + kk * 8, v_lo + kk * (16 * 128 >> 4),
-                 kIdO, !first_tile || kk > 0);
-      };
-      auto wait_p = [&](int s, int u) {
-        ok = mbar_wait(&p_full[s], u & 1, err, DFLASH_STATUS_TIMEOUT, abort_word);
-      };
+      bool any = false;  // MMAs of the first of this thread's streams
       if (PAIR) {
-        if (ok) {
-          const int sl = wait_entry();
-          if (ok) {
-            scores(0, sl);
-            scores(1, sl);
-          }
-        }
 #pragma unroll 1
-        for (int t = 0; t < nt && ok; ++t) {
-          const bool more = t + 1 < nt;
-          int ks = 0;
-          const int vs = wait_entry();
-          if (ok && more) ks = wait_entry();
-          if (!ok) break;
-#pragma unroll 1
+        for (int u = -1; u < nt && ok; ++u) {
+          const uint32_t v = u >= 0 ? wait_tile() : 0u;
+          const bool more = u + 1 < nt;
+          const uint32_t k = ok && more ? wait_tile() : 0u;
+#pragma unroll
           for (int s = 0; s < 2; ++s) {
-            wait_p(s, t);
             if (!ok) break;
-            output(s, vs, t == 0);
-            if (more) scores(s, ks);
+            if (u >= 0) output(s, u, v);
+            if (ok && more) {
+              scores(s, k);
+              any = true;
+            }
           }
         }
       } else {
+        const int s = warp - kMma, n_mine = (nt + 1 - s) / 2;
 #pragma unroll 1
-        for (int t = 0; t < 2 && t < nt && ok; ++t) {
-          const int sl = wait_entry();
-          if (!ok) break;
-          scores(t, sl);
-        }
-#pragma unroll 1
-        for (int t = 0; t < nt && ok; ++t) {
-          const int s = t & 1, vs = wait_entry();
-          if (ok) wait_p(s, t >> 1);
-          if (!ok) break;
-          output(s, vs, t < 2);
-          if (t + 2 < nt) {
-            const int ks = wait_entry();
+        for (int u = -1; u < n_mine && ok; ++u) {
+          if (u >= 0) {
+            const uint32_t v = wait_tile();
+            if (ok) output(s, u, v);
+          }
+          if (ok && u + 1 < n_mine) {
+            const uint32_t k = wait_tile();
             if (!ok) break;
-            scores(s, ks);
+            scores(s, k);
+            any = true;
           }
         }
       }
       // every MMA completes before tensor memory is read for the last time or released
       if (any) {
-        umma_commit(o_full);
-        mbar_wait(o_full, 0, err, DFLASH_STATUS_TIMEOUT, nullptr);
+        const int s = warp - kMma;
+        umma_commit(&o_full[s]);
+        if (PAIR) umma_commit(&o_full[1]);
+        mbar_wait(&o_full[s], 0, err, DFLASH_STATUS_TIMEOUT, nullptr);
       }
     }
     __syncwarp();
-  } else if (warp > kMma && !FP4) {
+  } else if (warp >= kProducer && !FP4) {
     // ------------------------------------------------ TMA producers, one warp for K and one for V: a lane a box
-    const int kv = warp - kMma - 1;
+    const int kv = warp - kProducer;
     const int boxes = kTK / a.c.page;  // boxes of 64 dims a tile: boxes * D / 64 <= 16
     const int b = lane % boxes, half = lane / boxes;
     int last = -1;
@@ -420,9 +434,9 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
     };
     int pg = lookup(0);
     for (int t = 0; t < nt; ++t) {
-      const int e = entry_of(kv, t), sl = e % kSlots;
+      const int sl = slot_of(kv, t), phase = phase_of(kv, t);
       const int next = lookup(t + 1);
-      bool ok = e < kSlots || mbar_wait(&empty[sl], ((e / kSlots) & 1) ^ 1u, err, DFLASH_STATUS_TIMEOUT, abort_word);
+      bool ok = phase == 0 || mbar_wait(&empty[sl], (phase & 1) ^ 1u, err, DFLASH_STATUS_TIMEOUT, abort_word);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const int kb = slot0(t);
@@ -456,15 +470,13 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
     // After a failure give those still in flight a millisecond (a slot that has
     // moved on since looks like one of them): the slots are used again below.
     if (last < nt - 1 || *reinterpret_cast<volatile int*>(abort_word))
-      for (int t = max(0, last - kSlots); t <= last; ++t) {
-        const int e = entry_of(kv, t);
-        mbar_wait(&full[e % kSlots], (e / kSlots) & 1, nullptr, 0, nullptr, 2000000);
-      }
-  } else if (FP4 && warp > kMma) {
+      for (int t = max(0, last - kSlots); t <= last; ++t)
+        mbar_wait(&full[slot_of(kv, t)], phase_of(kv, t) & 1, nullptr, 0, nullptr, 2000000);
+  } else if (FP4 && warp >= kProducer) {
     // ------------------------------------------------ 4-bit producers: a thread a key
     if constexpr (FP4) {
     constexpr int kSt = Ge::kStage;
-    const int key = static_cast<int>(threadIdx.x) - (kSoftThreads + 32);
+    const int key = static_cast<int>(threadIdx.x) - 32 * kProducer;
     const uint32_t raw_u = sbase + Ge::kOffRaw + key * Ge::kRow;
     const uint8_t* raw = smem + Ge::kOffRaw + key * Ge::kRow;
     constexpr int kPieces = Ge::kRow / 16;
@@ -502,9 +514,10 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
     for (int e = 0; e < entries; ++e) {
       stage(e + kSt - 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(kSt - 1) : "memory");
-      const int sl = e % kSlots;
-      const bool ok =
-          e < kSlots || mbar_wait(&empty[sl], ((e / kSlots) & 1) ^ 1u, err, DFLASH_STATUS_TIMEOUT, abort_word);
+      int kv, t;
+      entry(e, &kv, &t);
+      const int sl = slot_of(kv, t), phase = phase_of(kv, t);
+      const bool ok = phase == 0 || mbar_wait(&empty[sl], (phase & 1) ^ 1u, err, DFLASH_STATUS_TIMEOUT, abort_word);
       if (!ok) break;
       const bool there = (have >> (kSt - 1)) & 1u;
       const uint8_t* src = raw + (e % kSt) * Ge::kRaw;
@@ -611,20 +624,20 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
       ok = mbar_wait(&s_full[s], u & 1, err, DFLASH_STATUS_TIMEOUT, abort_word);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      // These scores are complete, and so is every MMA issued before them: the
+      // These scores are complete, and so is every MMA of the stream before them: the
       // slot of their K is free, and that of the V before. (Said here: a commit
       // of its own would cost the issuing thread the time of one and a half MMAs.)
-      if (q4 == 0 && lane == 0 && (!PAIR || s == 1)) {
-        const int t = PAIR ? u : 2 * u + s, tv = PAIR ? t - 1 : t - 2;
-        mbar_arrive(&empty[entry_of(0, t) % kSlots]);
-        if (tv >= 0) mbar_arrive(&empty[entry_of(1, tv) % kSlots]);
+      if (q4 == 0 && lane == 0) {
+        const int t = tile_of(s, u), tv = PAIR ? t - 1 : t - 2;
+        mbar_arrive(&empty[slot_of(0, t)]);
+        if (tv >= 0) mbar_arrive(&empty[slot_of(1, tv)]);
       }
       if (idle) {
-        if (lane == 0) mbar_arrive(&p_full[s]);
+        if (lane < Ge::kParts) mbar_arrive(&p_full[2 * s + lane]);
         continue;
       }
       tc_fence_after();
-      const int kb = slot0(PAIR ? u : 2 * u + s);
+      const int kb = slot0(tile_of(s, u));
       const bool whole = kb + kTK <= all_end && (kb >= lo_max || kb + kTK <= sinks);
       uint32_t vis[4];
       if (!whole) {
@@ -670,32 +683,32 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
             if (!((vis[c] >> i) & 1u)) x[i] = -INFINITY;
         }
       };
-      float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
-      auto most = [&](const float* x) {
+      // (the load itself gives the largest of its 32 scores)
+      float tm[4];
+      auto load_max = [&](int c, float* x) {
+        tmem_ld32_max(ts + c * 32, reinterpret_cast<uint32_t*>(x), tm[c]);
+      };
+      auto hidden_max = [&](int c, float* x) {
+        if (!whole) {
+          hide(c, x);
+          tm[c] = x[0];
 #pragma unroll
-        for (int i = 0; i < 32; i += 8) {
-          t0 = max3(t0, x[i], x[i + 1]);
-          t1 = max3(t1, x[i + 2], x[i + 3]);
-          t2 = max3(t2, x[i + 4], x[i + 5]);
-          t3 = max3(t3, x[i + 6], x[i + 7]);
+          for (int i = 1; i < 31; i += 2) tm[c] = max3(tm[c], x[i], x[i + 1]);
+          tm[c] = fmaxf(tm[c], x[31]);
         }
       };
 #pragma unroll
       for (int c = kHold; c < 4; ++c) {
-        load_scores(c, sv);
+        load_max(c, sv);
         tmem_wait_ld();
-        hide(c, sv);
-        most(sv);
+        hidden_max(c, sv);
       }
 #pragma unroll
-      for (int c = 0; c < kHold; ++c) load_scores(c, sv + c * 32);
+      for (int c = 0; c < kHold; ++c) load_max(c, sv + c * 32);
       tmem_wait_ld();
 #pragma unroll
-      for (int c = 0; c < kHold; ++c) {
-        hide(c, sv + c * 32);
-        most(sv + c * 32);
-      }
-      const float top = max3(max3(t0, t1, t2), t3, t3) * sc;
+      for (int c = 0; c < kHold; ++c) hidden_max(c, sv + c * 32);
+      const float top = max3(max3(tm[0], tm[1], tm[2]), tm[3], tm[3]) * sc;
       // The scores are complete, so every output product before them is too:
       // the output may be rescaled in place.
       const bool need = top > m + kRescale;
@@ -740,21 +753,23 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
           pk[i / 2 + 1] = pack2<FP4>(x[i + 2], x[i + 3]);
         }
         tmem_st16(ts + c * 16, pk);
+        if (Ge::kParts == 2 ? c & 1 : c == 3) {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * s + (Ge::kParts == 2 ? c >> 1 : 0)]);
+        }
       }
       float a0, a1;
       untwo(add2(sum0, sum1), a0, a1);
       l += a0 + a1;
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[s]);
     }
     // ------------------------------------------------ output
-    if (nt > 0) {
-      ok = ok && mbar_wait(o_full, 0, err, DFLASH_STATUS_TIMEOUT, abort_word);
-      ok = __all_sync(0xffffffffu, ok);
-      tc_fence_after();
-    }
+    // (the second stream's rows go through the ring: both streams' MMAs must be done)
+    if (n_mine > 0) ok = ok && mbar_wait(&o_full[s], 0, err, DFLASH_STATUS_TIMEOUT, abort_word);
+    if (!PAIR && s == 1 && nt > 0) ok = mbar_wait(&o_full[0], 0, err, DFLASH_STATUS_TIMEOUT, abort_word) && ok;
+    ok = __all_sync(0xffffffffu, ok);
+    tc_fence_after();
     const bool mine = ok && n_mine > 0 && !idle;
     float* xo = reinterpret_cast<float*>(smem + Ge::kOffSlots);  // [128][kPartLd] the second stream's rows
     float* xm = xo + kMRows * Ge::kPartLd;                       // [128][2]
