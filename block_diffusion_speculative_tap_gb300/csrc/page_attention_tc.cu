@@ -19,8 +19,8 @@
 // first tiles.
 //
 // Keys come in tiles of 128 through a ring of slots, K and V alternating: bf16
-// pages by TMA, one box a page and 64 dims; 4-bit pages by four warps, a
-// thread a key: cp.async into a private staging row, codes and scales to fp16
+// pages by TMA, one box a page and 64 dims, a warp each for K and V; 4-bit pages
+// by four warps each, a thread a key: cp.async into a private staging row, codes and scales to fp16
 // in registers, 16-byte stores into the swizzled slot.
 //
 // V rows of slots that no row of the tile sees are zeroed in the slot (a
@@ -46,14 +46,14 @@ constexpr int kProducer = kMma + 2;
 
 template <int D, bool FP4, bool PAIR>
 struct TcGeo {
-  static constexpr int kProd = FP4 ? 4 : 2;                 // producer warps (bf16: K, V)
+  static constexpr int kProd = FP4 ? 8 : 2;                 // producer warps, half for K and half for V
   static constexpr int kThreads = kSoftThreads + 64 + 32 * kProd;
   static constexpr int kSub = kTK * 128;                    // 128 rows x 64 dims
   static constexpr int kSlot = kTK * D * 2;                 // a K or V tile
   static constexpr int kQ = (PAIR ? 2 : 1) * kMRows * D * 2;
   static constexpr int kRow = D / 2, kSc = D / 16;          // 4-bit row and scale bytes
   static constexpr int kRaw = FP4 ? kTK * (kRow + (kSc > 8 ? kSc : 8)) : 0;  // a staged 4-bit tile
-  static constexpr int kStage = FP4 ? (PAIR ? 3 : 6) : 0;   // staged tiles
+  static constexpr int kStage = FP4 ? (PAIR && D == 128 ? 2 : 6) : 0;  // staged tiles, half for K and half for V
   static constexpr int kSlots = D == 64 ? 8 : FP4 ? 4 : (PAIR ? 5 : 6);
   static constexpr int kOffSlots = kQ;
   static constexpr int kOffRaw = kOffSlots + kSlots * kSlot;
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
   }
   if (threadIdx.x == 32) {
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&full[s], FP4 ? 32 * Ge::kProd : 1);
+      mbar_init(&full[s], FP4 ? kTK : 1);
       mbar_init(&empty[s], PAIR ? 2 : 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -310,16 +310,9 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
   // thread that waits on it: no thread is ever more than one phase away.
   // K of tile t is the ring's use 2u, its V the use 2u + 1 (u = t, or t / 2).
   constexpr int kRing = PAIR ? kSlots : kSlots / 2;
-  const int entries = 2 * nt;
   auto use_of = [&](int kv, int t) { return 2 * (PAIR ? t : t >> 1) + kv; };
   auto slot_of = [&](int kv, int t) { return (PAIR ? 0 : (t & 1) * kRing) + use_of(kv, t) % kRing; };
   auto phase_of = [&](int kv, int t) { return use_of(kv, t) / kRing; };
-  // One producer's order (4-bit pages): pair K0 V0 K1 V1 ..; parity K0 K1 V0 V1 K2 K3 ..
-  auto entry = [&](int e, int* kv, int* t) {
-    const bool both = !PAIR && (e | 3) < entries;  // the group of four has two tiles
-    *kv = both ? (e >> 1) & 1 : e & 1;
-    *t = PAIR ? e >> 1 : 2 * (e >> 2) + (both ? e & 1 : 0);
-  };
   auto tile_of = [&](int s, int u) { return PAIR ? u : 2 * u + s; };  // a stream's key tiles
 
   if (warp == kMma || warp == kMma + 1) {
@@ -473,56 +466,62 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
       for (int t = max(0, last - kSlots); t <= last; ++t)
         mbar_wait(&full[slot_of(kv, t)], phase_of(kv, t) & 1, nullptr, 0, nullptr, 2000000);
   } else if (FP4 && warp >= kProducer) {
-    // ------------------------------------------------ 4-bit producers: a thread a key
+    // ------------------------------------------------ 4-bit producers: four warps for K and four for V, a thread a key
     if constexpr (FP4) {
-    constexpr int kSt = Ge::kStage;
-    const int key = static_cast<int>(threadIdx.x) - 32 * kProducer;
-    const uint32_t raw_u = sbase + Ge::kOffRaw + key * Ge::kRow;
-    const uint8_t* raw = smem + Ge::kOffRaw + key * Ge::kRow;
+    constexpr int kSt = Ge::kStage / 2;
+    const int kv = (warp - kProducer) >> 2;
+    const int key = static_cast<int>(threadIdx.x) - 32 * kProducer - kTK * kv;
+    const uint32_t raw0 = Ge::kOffRaw + kv * kSt * Ge::kRaw;
+    const uint32_t raw_u = sbase + raw0 + key * Ge::kRow;
+    const uint8_t* raw = smem + raw0 + key * Ge::kRow;
     constexpr int kPieces = Ge::kRow / 16;
     auto swp = [&](int c) { return kPieces == 4 ? c ^ ((key >> 1) & 3) : c ^ ((key >> 2) & 1); };
+    const uint8_t* pool = kv ? a.c.v : a.c.k;
+    const uint8_t* spool = kv ? a.c.vs : a.c.ks;
     uint32_t have = 0;  // staged tiles in flight, newest in bit 0: this thread's key is there
-    auto stage = [&](int e) {
+    // the page of this thread's key of a tile, looked up a tile ahead
+    auto lookup = [&](int t) -> int {
+      if (t >= nt) return -1;
+      const int slot = slot0(t) + key;
+      if (!live(slot)) return -1;
+      const int pg = page_of(slot);
+      if (pg < 0) flag_status(err, DFLASH_STATUS_BAD_PAGE);
+      return pg;
+    };
+    int pre = lookup(0);
+    auto stage = [&](int t) {
       have <<= 1;
-      if (e < entries) {
-        int kv, t;
-        entry(e, &kv, &t);
-        const int slot = slot0(t) + key;
-        const int pg = live(slot) ? page_of(slot) : -1;
-        if (pg >= 0) {
-          have |= 1u;
-          const int64_t row = (static_cast<int64_t>(pg) * a.c.nkv + h) * a.c.page + (slot & (a.c.page - 1));
-          const uint8_t* src = (kv ? a.c.v : a.c.k) + row * Ge::kRow;
-          const uint8_t* ssc = (kv ? a.c.vs : a.c.ks) + row * Ge::kSc;
-          const uint32_t d0 = raw_u + (e % kSt) * Ge::kRaw;
+      const int pg = pre;
+      pre = lookup(t + 1);
+      if (pg >= 0) {
+        have |= 1u;
+        const int64_t row =
+            (static_cast<int64_t>(pg) * a.c.nkv + h) * a.c.page + ((slot0(t) + key) & (a.c.page - 1));
+        const uint8_t* src = pool + row * Ge::kRow;
+        const uint32_t d0 = raw_u + (t % kSt) * Ge::kRaw;
 #pragma unroll
-          for (int c = 0; c < kPieces; ++c)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d0 + swp(c) * 16), "l"(src + c * 16)
-                         : "memory");
-          const uint32_t ds = sbase + Ge::kOffRaw + (e % kSt) * Ge::kRaw + kTK * Ge::kRow + key * 8;
-          if (Ge::kSc == 8)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(ds), "l"(ssc) : "memory");
-          else
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ds), "l"(ssc) : "memory");
-        } else if (live(slot)) {
-          flag_status(err, DFLASH_STATUS_BAD_PAGE);
-        }
+        for (int c = 0; c < kPieces; ++c)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d0 + swp(c) * 16), "l"(src + c * 16)
+                       : "memory");
+        const uint32_t ds = sbase + raw0 + (t % kSt) * Ge::kRaw + kTK * Ge::kRow + key * 8;
+        if (Ge::kSc == 8)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(ds), "l"(spool + row * Ge::kSc) : "memory");
+        else
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ds), "l"(spool + row * Ge::kSc) : "memory");
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    for (int e = 0; e + 1 < kSt; ++e) stage(e);
-    for (int e = 0; e < entries; ++e) {
-      stage(e + kSt - 1);
+    for (int t = 0; t + 1 < kSt; ++t) stage(t);
+    for (int t = 0; t < nt; ++t) {
+      stage(t + kSt - 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(kSt - 1) : "memory");
-      int kv, t;
-      entry(e, &kv, &t);
       const int sl = slot_of(kv, t), phase = phase_of(kv, t);
       const bool ok = phase == 0 || mbar_wait(&empty[sl], (phase & 1) ^ 1u, err, DFLASH_STATUS_TIMEOUT, abort_word);
       if (!ok) break;
       const bool there = (have >> (kSt - 1)) & 1u;
-      const uint8_t* src = raw + (e % kSt) * Ge::kRaw;
+      const uint8_t* src = raw + (t % kSt) * Ge::kRaw;
       const uint32_t* scp =
-          reinterpret_cast<const uint32_t*>(smem + Ge::kOffRaw + (e % kSt) * Ge::kRaw + kTK * Ge::kRow + key * 8);
+          reinterpret_cast<const uint32_t*>(smem + raw0 + (t % kSt) * Ge::kRaw + kTK * Ge::kRow + key * 8);
       uint32_t sw[2] = {0u, 0u};  // a key that is not there: all its values are zero
       if (there) {
         sw[0] = scp[0];
