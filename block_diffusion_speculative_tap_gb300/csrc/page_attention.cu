@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int j = static_cast<int>(static_cast<unsigned>(sg.tile * kTile + 8 * b + 2 * t + i) / a.G);
+      const int j = by_group(a, static_cast<unsigned>(sg.tile * kTile + 8 * b + 2 * t + i));
       RowView& v = rv[b][i];
       v.j = j < q.n ? j : -1;
       v.pos = v.j >= 0 ? row_pos(a.r, q, j) : 0;
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     const unsigned f = static_cast<unsigned>(sg.tile * kTile + 8 * b + g);
-    const int j = static_cast<int>(f / a.G), hd = static_cast<int>(f - j * a.G);
+    const int j = by_group(a, f), hd = static_cast<int>(f - j * a.G);
     const __nv_bfloat16* qp =
         j < q.n ? a.q + static_cast<int64_t>(q.row0 + j) * a.q_ld + (h * a.G + hd) * D : nullptr;
     constexpr int kPieces = D / 32;  // 16-byte pieces of a row a lane holds
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
   for (int x = threadIdx.x; x < kTile * (D / 4); x += kWarps * 32) {
     const int r = x / (D / 4), d4 = (x % (D / 4)) * 4;
     const unsigned f = static_cast<unsigned>(sg.tile * kTile + r);
-    const int j = static_cast<int>(f / a.G);
+    const int j = by_group(a, f);
     if (j >= q.n) continue;
     float M = -INFINITY;
 #pragma unroll
@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(kCombineRows * 32) page_combine_kernel(const _
   if (jr.parts == 0) return;
   const int r = blockIdx.y * kCombineRows + warp;
   const unsigned f = jr.f0 + r;
-  const int j = static_cast<int>(f / a.G);
+  const int j = by_group(a, f);
   if (r >= a.tile || j >= jr.n) return;
   auto row_of = [&](int k) { return static_cast<int64_t>(k == 0 ? jr.slot : 2 * (b + k - 1)) * a.tile + r; };
   float M = -INFINITY, den = 0.f;
@@ -703,7 +703,7 @@ __global__ void __launch_bounds__(D * 4) page_combine_tile_kernel(const __grid_c
   if (jr.parts == 0) return;
   const int r = blockIdx.y * kCombineTile + lane;
   const unsigned f = jr.f0 + r;
-  const int j = static_cast<int>(f / a.G);
+  const int j = by_group(a, f);
   if (j >= jr.n) return;
   auto slot_of = [&](int k) { return static_cast<int64_t>(k == 0 ? jr.slot : 2 * (b + k - 1)) * a.tile; };
   float M = -INFINITY, den = 0.f;
@@ -779,13 +779,15 @@ PagePlan page_attention_plan(const dflash_pages& c, const dflash_rows& r, int nq
     p.tile = R > 512 ? 256 : 128;
     p.unit = 128;
     p.target = 152;
-    p.min_units = 4;
+    p.over = 4;
+    p.min_units = 4 + 4;
     p.no_split = 4;
   } else {
     p.tile = R > 8 ? 16 : 8;
     p.unit = fp4 ? 32 : 16;
     p.target = 152 * (fp4 ? 2 : 1);
-    p.min_units = 2 * kWarps;
+    p.over = 8;
+    p.min_units = 8 + 2 * kWarps;
     p.no_split = 4 * kWarps;
   }
   const int64_t per_stream = (R + p.tile - 1) / p.tile;
@@ -793,7 +795,7 @@ PagePlan page_attention_plan(const dflash_pages& c, const dflash_rows& r, int nq
   const int64_t tiles = std::min(c.streams * per_stream, by_rows) * c.n_kv_heads;
   const int64_t units = (static_cast<int64_t>(c.table_cols) * c.page_size + p.unit - 1) / p.unit;
   // (places on the line of all units are 31 bits wide)
-  p.split = units > p.no_split && c.streams * per_stream * c.n_kv_heads < 0x7fffffff / units;
+  p.split = units > p.no_split && c.streams * per_stream * c.n_kv_heads < 0x7fffffff / (units + p.over);
   p.ctas = std::max<int64_t>(tiles, p.split ? p.target : 0);
   return p;
 }

@@ -41,13 +41,13 @@ constexpr int kMRows = 128;              // rows of a softmax stream
 constexpr float kRescale = 8.f;          // log2 by which the maximum in use may lag
 constexpr int kSoftWarps = 8;            // two streams x four lane quadrants
 constexpr int kSoftThreads = 32 * kSoftWarps;
-constexpr int kMma = kSoftWarps;         // two MMA warps; the producers follow
-constexpr int kProducer = kMma + 2;
+constexpr int kMma = kSoftWarps;         // the MMA warp; the producers follow
+constexpr int kProducer = kMma + 1;
 
 template <int D, bool FP4, bool PAIR>
 struct TcGeo {
   static constexpr int kProd = FP4 ? 8 : 2;                 // producer warps, half for K and half for V
-  static constexpr int kThreads = kSoftThreads + 64 + 32 * kProd;
+  static constexpr int kThreads = kSoftThreads + 32 + 32 * kProd;
   static constexpr int kSub = kTK * 128;                    // 128 rows x 64 dims
   static constexpr int kSlot = kTK * D * 2;                 // a K or V tile
   static constexpr int kQ = (PAIR ? 2 : 1) * kMRows * D * 2;
@@ -60,8 +60,6 @@ struct TcGeo {
   static constexpr int kOffBar = kOffRaw + kStage * kRaw;
   static constexpr int kSmem = kOffBar + 512;
   static constexpr int kHold = !FP4 && PAIR ? 2 : 1;  // of a tile's four chunks of 32 scores, those kept in registers
-  static constexpr int kParts = PAIR ? 1 : 2;         // P is handed on whole, or 64 keys at a time
-  static constexpr int kIssuers = PAIR ? 1 : 2;       // threads that issue MMAs
   static constexpr int kPartLd = D + 4;
   static constexpr int kColO = 256;
   static constexpr float kShift = FP4 ? 7.f : 0.f;  // P <= 2^(kRescale + kShift) in fp16
@@ -238,10 +236,10 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Ge::kOffBar);  // [kSlots] a tile is in its slot
   uint64_t* empty = full + kSlots;   // [kSlots] the MMAs that read the slot are done (a softmax thread of each reader says so)
   uint64_t* s_full = empty + kSlots; // [2] a stream's scores are in tensor memory
-  uint64_t* p_full = s_full + 2;     // [2][2] its weights are (of 64 keys, or all), and its output is rescaled
-  uint64_t* q_full = p_full + 4;     // the queries are in shared memory
-  uint64_t* o_full = q_full + 1;     // [2] every MMA of a stream is done
-  uint64_t* landed = o_full + 2;     // a tile that has to be cleaned is in its slot
+  uint64_t* p_full = s_full + 2;     // [2] its weights are, and its output is rescaled
+  uint64_t* q_full = p_full + 2;     // the queries are in shared memory
+  uint64_t* o_full = q_full + 1;     // every MMA is done
+  uint64_t* landed = o_full + 1;     // a tile that has to be cleaned is in its slot
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(landed + 1);
   int* abort_word = reinterpret_cast<int*>(tmem_slot + 1);
   Run* run = reinterpret_cast<Run*>(smem + Ge::kOffBar + 256);
@@ -265,12 +263,10 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[2 * s], kSoftWarps / 2);
-      mbar_init(&p_full[2 * s + 1], kSoftWarps / 2);
+      mbar_init(&p_full[s], kSoftWarps / 2);
     }
     mbar_init(q_full, PAIR ? kSoftWarps : kSoftWarps / 2);
-    mbar_init(&o_full[0], 1);
-    mbar_init(&o_full[1], 1);
+    mbar_init(o_full, 1);
     mbar_init(landed, 1);
     if (first) *abort_word = 0;
     fence_barrier_init();
@@ -315,45 +311,37 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
   auto phase_of = [&](int kv, int t) { return use_of(kv, t) / kRing; };
   auto tile_of = [&](int s, int u) { return PAIR ? u : 2 * u + s; };  // a stream's key tiles
 
-  if (warp == kMma || warp == kMma + 1) {
-    // ------------------------------------------------ MMA issuers
-    // Issuing takes as long as the MMAs run, and a wait that is over at once
-    // still takes 100 cycles. Parity: a thread a stream, so that one waits while
-    // the other issues (blocks 62 -> 60 us, trees 130 -> 122 us). Pair: one thread
-    // for both, since there the streams' MMAs in turn would double the time until
-    // either's scores are ready (a 4096-row chunk: 367 us with one, 408 us with two).
-    if (lane == 0 && warp - kMma < Ge::kIssuers) {
+  if (warp == kMma) {
+    // ------------------------------------------------ MMA issuer: one thread, and little code
+    // Issuing takes as long as the MMAs run (64 cycles each), and whatever the
+    // thread does in between the tensor cores stand still for: a wait that is
+    // over at once takes 100 cycles, a commit as long as one and a half MMAs.
+    if (lane == 0) {
       constexpr uint32_t kIdS = idesc16(FP4, kMRows, kTK, false);
       constexpr uint32_t kIdO = idesc16(FP4, kMRows, D, true);
       const uint32_t slots = sbase + Ge::kOffSlots;
       bool ok = nt > 0 && mbar_wait(q_full, 0, err, DFLASH_STATUS_TIMEOUT, abort_word);
-      // the next use of this thread's ring
-      uint32_t ring = slots + (PAIR ? 0 : (warp - kMma) * kRing * Ge::kSlot), at = 0, parity = 0;
-      uint64_t* ring_full = full + (PAIR ? 0 : (warp - kMma) * kRing);
-      auto wait_tile = [&]() -> uint32_t {
-        ok = mbar_wait(&ring_full[at], parity, err, DFLASH_STATUS_TIMEOUT, abort_word);
-        const uint32_t tile = ring + at * Ge::kSlot;
-        if (++at == kRing) {
-          at = 0;
-          parity ^= 1u;
+      // the next use of a ring (of the one, or of stream s's)
+      int at[2] = {0, 0};
+      uint32_t parity[2] = {0u, 0u};
+      auto wait_tile = [&](int s) -> uint32_t {
+        const int sl = s * kRing + at[s];
+        ok = mbar_wait(&full[sl], parity[s], err, DFLASH_STATUS_TIMEOUT, abort_word);
+        if (++at[s] == kRing) {
+          at[s] = 0;
+          parity[s] ^= 1u;
         }
-        return tile;
+        return slots + sl * Ge::kSlot;
       };
-      // O (+)= P V of the stream's tile u, as its weights come
+      // O (+)= P V of the stream's tile u
       auto output = [&](int s, int u, uint32_t v) {
         const uint32_t v_lo = desc_lo(v, Ge::kSub >> 4);
+        ok = mbar_wait(&p_full[s], u & 1, err, DFLASH_STATUS_TIMEOUT, abort_word);
+        if (!ok) return;
+        tc_fence_after();
 #pragma unroll
-        for (int hf = 0; hf < Ge::kParts; ++hf) {
-          if (ok) ok = mbar_wait(&p_full[2 * s + hf], u & 1, err, DFLASH_STATUS_TIMEOUT, abort_word);
-          if (!ok) return;
-          tc_fence_after();
-#pragma unroll
-          for (int k4 = 0; k4 < kTK / 16 / Ge::kParts; ++k4) {
-            const int kk = hf * (kTK / 32) + k4;
-            mma_ts(tmem + Ge::kColO + s * D, tmem + s * 128 + kk * 8, v_lo + kk * (16 * 128 >> 4), kIdO,
-                   u > 0 || kk > 0);
-          }
-        }
+        for (int kk = 0; kk < kTK / 16; ++kk)
+          mma_ts(tmem + Ge::kColO + s * D, tmem + s * 128 + kk * 8, v_lo + kk * (16 * 128 >> 4), kIdO, u > 0 || kk > 0);
       };
       // S = Q K^T of its next tile, behind the product that still reads P there
       auto scores = [&](int s, uint32_t k) {
@@ -367,45 +355,36 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
         }
         umma_commit(&s_full[s]);
       };
-      bool any = false;  // MMAs of the first of this thread's streams
-      if (PAIR) {
+      const bool any = ok;  // (a commit with nothing before it completes at once)
 #pragma unroll 1
-        for (int u = -1; u < nt && ok; ++u) {
-          const uint32_t v = u >= 0 ? wait_tile() : 0u;
+      for (int u = -1; tile_of(0, u) < nt && ok; ++u) {
+        if (PAIR) {
+          const uint32_t v = u >= 0 ? wait_tile(0) : 0u;
           const bool more = u + 1 < nt;
-          const uint32_t k = ok && more ? wait_tile() : 0u;
+          const uint32_t k = ok && more ? wait_tile(0) : 0u;
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
-            if (!ok) break;
-            if (u >= 0) output(s, u, v);
-            if (ok && more) {
-              scores(s, k);
-              any = true;
+            if (ok && u >= 0) output(s, u, v);
+            if (ok && more) scores(s, k);
+          }
+        } else {
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (ok && u >= 0 && tile_of(s, u) < nt) {
+              const uint32_t v = wait_tile(s);
+              if (ok) output(s, u, v);
             }
-          }
-        }
-      } else {
-        const int s = warp - kMma, n_mine = (nt + 1 - s) / 2;
-#pragma unroll 1
-        for (int u = -1; u < n_mine && ok; ++u) {
-          if (u >= 0) {
-            const uint32_t v = wait_tile();
-            if (ok) output(s, u, v);
-          }
-          if (ok && u + 1 < n_mine) {
-            const uint32_t k = wait_tile();
-            if (!ok) break;
-            scores(s, k);
-            any = true;
+            if (ok && tile_of(s, u + 1) < nt) {
+              const uint32_t k = wait_tile(s);
+              if (ok) scores(s, k);
+            }
           }
         }
       }
       // every MMA completes before tensor memory is read for the last time or released
       if (any) {
-        const int s = warp - kMma;
-        umma_commit(&o_full[s]);
-        if (PAIR) umma_commit(&o_full[1]);
-        mbar_wait(&o_full[s], 0, err, DFLASH_STATUS_TIMEOUT, nullptr);
+        umma_commit(o_full);
+        mbar_wait(o_full, 0, err, DFLASH_STATUS_TIMEOUT, nullptr);
       }
     }
     __syncwarp();
@@ -558,7 +537,7 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
     const uint32_t ts = tl + s * 128, to = tl + Ge::kColO + s * D;
     const unsigned f = f0 + (PAIR ? s * kMRows : 0) + r;
     RowView rv;
-    const int jr = static_cast<int>(f / a.G);
+    const int jr = by_group(a, f);
     const int hd = static_cast<int>(f - jr * a.G);
     rv.j = jr < q.n ? jr : -1;
     rv.pos = rv.j >= 0 ? row_pos(a.r, q, jr) : 0;
@@ -624,15 +603,15 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       // These scores are complete, and so is every MMA of the stream before them: the
-      // slot of their K is free, and that of the V before. (Said here: a commit
-      // of its own would cost the issuing thread the time of one and a half MMAs.)
+      // slot of their K is free, and that of the V before. (Said here: the issuing
+      // thread would have to commit once more.)
       if (q4 == 0 && lane == 0) {
         const int t = tile_of(s, u), tv = PAIR ? t - 1 : t - 2;
         mbar_arrive(&empty[slot_of(0, t)]);
         if (tv >= 0) mbar_arrive(&empty[slot_of(1, tv)]);
       }
       if (idle) {
-        if (lane < Ge::kParts) mbar_arrive(&p_full[2 * s + lane]);
+        if (lane == 0) mbar_arrive(&p_full[s]);
         continue;
       }
       tc_fence_after();
@@ -752,21 +731,17 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
           pk[i / 2 + 1] = pack2<FP4>(x[i + 2], x[i + 3]);
         }
         tmem_st16(ts + c * 16, pk);
-        if (Ge::kParts == 2 ? c & 1 : c == 3) {
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[2 * s + (Ge::kParts == 2 ? c >> 1 : 0)]);
-        }
       }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[s]);
       float a0, a1;
       untwo(add2(sum0, sum1), a0, a1);
       l += a0 + a1;
     }
     // ------------------------------------------------ output
-    // (the second stream's rows go through the ring: both streams' MMAs must be done)
-    if (n_mine > 0) ok = ok && mbar_wait(&o_full[s], 0, err, DFLASH_STATUS_TIMEOUT, abort_word);
-    if (!PAIR && s == 1 && nt > 0) ok = mbar_wait(&o_full[0], 0, err, DFLASH_STATUS_TIMEOUT, abort_word) && ok;
+    if (nt > 0) ok = ok && mbar_wait(o_full, 0, err, DFLASH_STATUS_TIMEOUT, abort_word);
     ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
     const bool mine = ok && n_mine > 0 && !idle;
@@ -779,12 +754,13 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
         xm[2 * r + 1] = mine ? l : 0.f;
         if (mine) {
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            float v[16];
-            tmem_ld16(to + c * 16, v);
+          for (int c = 0; c < D / 32; ++c) {
+            float v[32];
+            tmem_ld32(to + c * 32, reinterpret_cast<uint32_t*>(v));
+          tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; i += 4)
-              *reinterpret_cast<float4*>(xo + r * Ge::kPartLd + c * 16 + i) =
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<float4*>(xo + r * Ge::kPartLd + c * 32 + i) =
                   make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
           }
         }
@@ -805,20 +781,21 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
       const int trow = (PAIR ? s * kMRows : 0) + r;  // parts lie by columns of four dims: a warp's rows side by side
       __nv_bfloat16* dst = a.out + static_cast<int64_t>(q.row0 + jr) * a.out_ld + (h * a.G + hd) * D;
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        float v[16];
+      for (int c = 0; c < D / 32; ++c) {
+        float v[32];
         if (mine) {
-          tmem_ld16(to + c * 16, v);
+          tmem_ld32(to + c * 32, reinterpret_cast<uint32_t*>(v));
+          tmem_wait_ld();
         } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = 0.f;
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = w0 > 0.f ? v[i] * w0 : 0.f;
+        for (int i = 0; i < 32; ++i) v[i] = w0 > 0.f ? v[i] * w0 : 0.f;
         if (!PAIR && w1 > 0.f) {
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            const float4 x = *reinterpret_cast<const float4*>(xo + r * Ge::kPartLd + c * 16 + i);
+          for (int i = 0; i < 32; i += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(xo + r * Ge::kPartLd + c * 32 + i);
             v[i] = fmaf(x.x, w1, v[i]);
             v[i + 1] = fmaf(x.y, w1, v[i + 1]);
             v[i + 2] = fmaf(x.z, w1, v[i + 2]);
@@ -828,13 +805,13 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
         if (!write) continue;
         if (split) {
 #pragma unroll
-          for (int i = 0; i < 16; i += 4)
-            *reinterpret_cast<float4*>(a.part_o + part_row * D + ((c * 16 + i) / 4 * a.tile + trow) * 4) =
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(a.part_o + part_row * D + ((c * 32 + i) / 4 * a.tile + trow) * 4) =
                 make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         } else {
 #pragma unroll
-          for (int i = 0; i < 16; i += 8)
-            *reinterpret_cast<uint4*>(dst + c * 16 + i) =
+          for (int i = 0; i < 32; i += 8)
+            *reinterpret_cast<uint4*>(dst + c * 32 + i) =
                 make_uint4(pack2<false>(v[i] * inv, v[i + 1] * inv), pack2<false>(v[i + 2] * inv, v[i + 3] * inv),
                            pack2<false>(v[i + 4] * inv, v[i + 5] * inv), pack2<false>(v[i + 6] * inv, v[i + 7] * inv));
         }
@@ -842,8 +819,11 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
       if (split && write) *reinterpret_cast<float2*>(a.part_ml + (part_row + trow) * 2) = make_float2(M, den);
     }
   }
+  fence_async();  // rows were joined through the ring that TMA writes next
   tc_fence_before();
   __syncthreads();
+  // an expired wait ends the CTA: what is still in flight knows these barriers
+  if (*reinterpret_cast<volatile int*>(abort_word)) break;
   if (threadIdx.x == 32) {
     for (uint64_t* b = full; b <= landed; ++b)
       asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(b)) : "memory");

@@ -50,8 +50,11 @@ struct PageAttnArgs {
   int unit_log2;         // slots a unit of the split
   int tile, tile_log2;   // rows (query row x head of the group) a tile
   int target;            // CTAs of one wave
+  unsigned target_inv;   // 2^32 / target, rounded up
+  unsigned group_inv;    // see by_group
   int min_units;         // fewest units a CTA's share has
   int no_split;          // tiles of up to this many units are not split
+  int over;              // units a segment costs beside its keys (under min_units)
   float* part_o;         // [2 * target][tile][d] (tiles of 128 rows and more: [d / 4][tile][4]); null: nothing is split
   float* part_ml;        // [2 * target][tile][2]
   JoinRecord* join;      // [target]
@@ -94,19 +97,24 @@ __device__ __forceinline__ UnitRange unit_range(int lo, int hi, int sinks, int u
 // The split of a call's work, the same in every CTA of a call. Each stream of
 // n rows is mt tiles of `tile` (row, head) pairs; a tile's keys are the
 // stream's units. All tiles' units, kv head by kv head, stream by stream, make
-// one line, and CTA b of B takes the part [total * b / B, total * (b + 1) / B)
-// of it: streams of unequal length make equal shares. A share is a run of
-// segments, each (part of) one tile; a part goes to the workspace, slot 2b for
-// a CTA's first segment and 2b + 1 for its last, and page_combine_kernel joins
-// the parts. With many tiles, or short ones, every CTA takes whole tiles
-// instead. Places on the line fit 31 bits (the host sees to it).
+// one line, and CTA b takes the part [b * per, (b + 1) * per) of it: streams of
+// unequal length make equal shares. A tile's place on the line begins with
+// `over` units that stand for what a segment costs beside its keys; a boundary
+// that falls on them is one at the tile's start. A share is a run of segments,
+// each (part of) one tile; a part goes to the workspace, slot 2b for a CTA's first segment
+// and 2b + 1 for its last, and the combine kernels join the parts. With many
+// tiles, or short ones, every CTA takes whole tiles instead. Places on the line
+// fit 31 bits (the host sees to it). This runs before anything else of a CTA,
+// by one warp and from a cold instruction cache, so it divides only where it
+// has to: 5600 cycles of a block's 100,000 with a division a step.
 struct Share {
   int line;    // units of a kv head (whole: its tiles)
-  int ctas;    // B
-  int q, r;    // total = q * B + r
-  bool whole;  // a tile a CTA
+  int total;   // of all of them
+  int per;     // a CTA's (whole: a tile)
+  bool whole;
   __device__ __forceinline__ int start(int b) const {
-    return whole ? b : q * b + static_cast<int>(static_cast<unsigned>(r * b) / static_cast<unsigned>(ctas));
+    const unsigned at = static_cast<unsigned>(per) * static_cast<unsigned>(b);
+    return at < static_cast<unsigned>(total) ? static_cast<int>(at) : total;
   }
 };
 
@@ -114,7 +122,7 @@ struct Share {
 struct Segment {
   int h, s, tile;     // kv head, stream, tile of it
   StreamRows q;       // the stream's rows
-  int u, x0, x1;      // units of the stream, and the part of them
+  int u, x0, x1;      // the tile's place on the line, and the part of it
   int j_lo, j_hi;     // first and last row of the tile
   int lo, lo_max, hi; // slots some row sees: from lo (all rows: from lo_max) to hi, and the sinks
   int sinks;
@@ -142,7 +150,7 @@ __device__ __forceinline__ LaneStream lane_stream(const PageAttnArgs& a, int s, 
   if (x.q.n == 0) return x;
   x.mt = (x.q.n * a.G + (1 << a.tile_log2) - 1) >> a.tile_log2;  // max_rows * G is under 2^31
   const int lo = a.window > 0 ? max(0, x.q.C - a.window + 1) : 0;
-  x.u = unit_range(lo, x.q.C + x.q.n, a.sinks, a.unit_log2).n;
+  x.u = unit_range(lo, x.q.C + x.q.n, a.sinks, a.unit_log2).n + a.over;
   return x;
 }
 
@@ -160,19 +168,18 @@ __device__ __forceinline__ Share share_of(const PageAttnArgs& a, LaneStream& las
   }
   Share sh;
   const unsigned all = tiles * a.c.nkv;
-  sh.whole = a.part_o == nullptr || most <= a.no_split || all >= 3u * a.target;
-  sh.q = sh.r = 0;
-  if (sh.whole) {
-    sh.line = static_cast<int>(tiles);
-    sh.ctas = static_cast<int>(all);
-  } else {
-    const unsigned total = line * a.c.nkv, b = (total + a.min_units - 1) / a.min_units;
-    sh.line = static_cast<int>(line);
-    sh.ctas = min(static_cast<int>(b), a.target);
-    sh.q = static_cast<int>(total / sh.ctas);
-    sh.r = static_cast<int>(total - sh.q * static_cast<unsigned>(sh.ctas));
-  }
+  sh.whole = a.part_o == nullptr || most <= a.no_split + a.over || all >= 3u * a.target;
+  sh.line = static_cast<int>(sh.whole ? tiles : line);
+  sh.total = sh.line * a.c.nkv;
+  // more than total / target (target_inv > 2^32 / target), so that no CTA past the target has work
+  const int fair = static_cast<int>(__umulhi(static_cast<unsigned>(sh.total), a.target_inv)) + 1;
+  sh.per = sh.whole ? 1 : max(a.min_units, fair);
   return sh;
+}
+
+// n / G for n under 2^25 (group_inv: 2^32 / G rounded up; 0 for G = 1).
+__device__ __forceinline__ int by_group(const PageAttnArgs& a, unsigned n) {
+  return static_cast<int>(a.group_inv ? __umulhi(n, a.group_inv) : n);
 }
 
 __device__ __forceinline__ int row_pos(const RowsArgs& r, const StreamRows& q, int j) {
@@ -182,14 +189,23 @@ __device__ __forceinline__ int row_pos(const RowsArgs& r, const StreamRows& q, i
 // The segment at place `at` of the line, `left` units (whole: a tile) at most.
 // One warp; false past the end. known: the lanes' streams, if they are at hand.
 __device__ __forceinline__ bool segment_at(const PageAttnArgs& a, const Share& sh, int at, int left,
-                                           bool have, const LaneStream& known, Segment* out) {
+                                           bool have, const LaneStream& known, Segment* out, int* next) {
   const int lane = threadIdx.x & 31;
   Segment g;
-  // whole tiles: every head's longest first
-  const int quot = static_cast<int>(static_cast<unsigned>(at) / static_cast<unsigned>(sh.whole ? a.c.nkv : sh.line));
-  const int rest = at - quot * (sh.whole ? a.c.nkv : sh.line);
-  g.h = sh.whole ? rest : quot;
-  const int r = sh.whole ? quot : rest;
+  int r = at;
+  if (sh.whole) {  // every head's longest first
+    r = static_cast<int>(static_cast<unsigned>(at) / static_cast<unsigned>(a.c.nkv));
+    g.h = at - r * a.c.nkv;
+  } else if (a.c.nkv <= 32) {
+    g.h = 0;
+    while (r >= sh.line) {
+      r -= sh.line;
+      ++g.h;
+    }
+  } else {
+    g.h = static_cast<int>(static_cast<unsigned>(at) / static_cast<unsigned>(sh.line));
+    r = at - g.h * sh.line;
+  }
   int base = 0;
   for (int s0 = 0; s0 < a.r.S; s0 += 32) {
     const LaneStream x = have ? known : lane_stream(a, s0 + lane, false);
@@ -213,13 +229,18 @@ __device__ __forceinline__ bool segment_at(const PageAttnArgs& a, const Share& s
     g.q.n = __shfl_sync(0xffffffffu, x.q.n, l);
     g.q.C = __shfl_sync(0xffffffffu, x.q.C, l);
     const int tiles = __shfl_sync(0xffffffffu, x.mt, l);
-    const int tile = sh.whole ? rel : static_cast<int>(static_cast<unsigned>(rel) / static_cast<unsigned>(g.u));
+    const int tile = sh.whole ? rel
+                     : tiles == 1 ? 0
+                                  : static_cast<int>(static_cast<unsigned>(rel) / static_cast<unsigned>(g.u));
     g.x0 = sh.whole ? 0 : rel - tile * g.u;
     g.x1 = sh.whole ? g.u : min(g.u, g.x0 + left);
+    *next = at + (sh.whole ? 1 : g.x1 - g.x0);
+    if (g.x1 < g.u && g.x1 <= a.over) return false;  // the next CTA's from the start
+    if (g.x0 <= a.over) g.x0 = 0;
     g.tile = tiles - 1 - tile;  // the last rows see most: whole tiles start with them
     const unsigned f0 = static_cast<unsigned>(g.tile) << a.tile_log2;
-    g.j_lo = static_cast<int>(f0 / static_cast<unsigned>(a.G));
-    g.j_hi = min(g.q.n - 1, static_cast<int>((f0 + (1u << a.tile_log2) - 1u) / static_cast<unsigned>(a.G)));
+    g.j_lo = by_group(a, f0);
+    g.j_hi = min(g.q.n - 1, by_group(a, f0 + (1u << a.tile_log2) - 1u));
     g.hi = g.q.C + (a.mode == DFLASH_MASK_CAUSAL ? g.j_hi + 1 : g.q.n);
     g.sinks = min(a.sinks, g.hi);
     g.lo = g.lo_max = 0;
@@ -240,14 +261,9 @@ __device__ __forceinline__ bool segment_at(const PageAttnArgs& a, const Share& s
       g.lo_max = max(0, p_hi - a.window + 1);
     }
     g.ur = unit_range(g.lo, g.hi, a.sinks, a.unit_log2);
-    g.i0 = 0;
-    g.i1 = g.ur.n;
-    // a tile's own units in the stream's proportion
-    if (g.x0 > 0 || g.x1 < g.u) {
-      const bool same = g.ur.n == g.u;
-      g.i0 = same ? g.x0 : static_cast<int>(static_cast<long long>(g.ur.n) * g.x0 / g.u);
-      g.i1 = same ? g.x1 : static_cast<int>(static_cast<long long>(g.ur.n) * g.x1 / g.u);
-    }
+    // a tile sees no more units than its stream: the rest of a part is empty
+    g.i0 = min(max(g.x0 - a.over, 0), g.ur.n);
+    g.i1 = g.x1 == g.u ? g.ur.n : min(g.x1 - a.over, g.ur.n);
     *out = g;
     return true;
   }
@@ -262,10 +278,8 @@ __device__ __forceinline__ void run_next(const PageAttnArgs& a, Run* run, bool b
   int at = 0, end = 0;
   if (begin) {
     sh = share_of(a, x);
-    if (static_cast<int>(blockIdx.x) < sh.ctas) {
-      at = sh.start(static_cast<int>(blockIdx.x));
-      end = sh.start(static_cast<int>(blockIdx.x) + 1);
-    }
+    at = sh.start(static_cast<int>(blockIdx.x));
+    end = sh.start(static_cast<int>(blockIdx.x) + 1);
     if (one) {
       run->sh = sh;
       run->end = end;
@@ -276,13 +290,14 @@ __device__ __forceinline__ void run_next(const PageAttnArgs& a, Run* run, bool b
     end = run->end;
   }
   Segment g;
-  const bool left = at < end && segment_at(a, sh, at, end - at, begin && a.r.S <= 32, x, &g);
+  int next = at;
+  const bool left = at < end && segment_at(a, sh, at, end - at, begin && a.r.S <= 32, x, &g, &next);
   __syncwarp();
   if (one) {
     run->left = left;
     if (left) {
       run->seg = g;
-      run->at = at + (sh.whole ? 1 : g.x1 - g.x0);
+      run->at = next;
     }
   }
 }
@@ -296,11 +311,9 @@ __device__ __forceinline__ void write_join(const PageAttnArgs& a, const Run& run
   if (run.left && g.x0 > 0) {  // the share starts inside a tile (never a CTA's first, nor with whole tiles)
     const Share& sh = run.sh;
     const int at = sh.start(b), from = at - g.x0, to = from + g.u, before = sh.start(b - 1);
-    if (before <= from) {  // the first boundary inside it
-      j.slot = 2 * (b - 1) + (before == from ? 0 : 1);
-      // the CTAs whose share starts before the tile's end: total * k / ctas < to, so k < to * ctas / total
-      const long long total = static_cast<long long>(sh.line) * a.c.nkv;
-      j.parts = static_cast<int>((static_cast<long long>(to) * sh.ctas + total - 1) / total) - (b - 1);
+    if (before <= from + a.over) {  // the first boundary inside it
+      j.slot = 2 * (b - 1) + (before >= from ? 0 : 1);
+      j.parts = (to - 1) / sh.per - (b - 1) + 1;  // the CTAs whose share starts before the tile's end
       j.h = g.h;
       j.row0 = g.q.row0;
       j.n = g.q.n;
@@ -340,7 +353,7 @@ int launch_page_read(const PagesArgs& c, const RowsArgs& r, __nv_bfloat16* k, in
 struct PagePlan {
   bool tc;      // the tensor-memory kernel
   bool split;   // tiles may be split: a workspace and a combine launch
-  int tile, unit, target, min_units, no_split;
+  int tile, unit, target, min_units, no_split, over;
   int64_t ctas;
 };
 PagePlan page_attention_plan(const dflash_pages& c, const dflash_rows& r, int nq);

@@ -85,8 +85,8 @@ size_t attention_ws(const PagePlan& p, const dflash_pages& c) {
 
 int check_heads(const dflash_pages* c, const dflash_rows* r, int nq) {
   if (nq < 1 || nq % c->n_kv_heads || nq / c->n_kv_heads > DFLASH_MAX_PAGE_GROUP) return DFLASH_E_SHAPE;
-  // a stream's (row, head of a group) pairs are counted in 31 bits, tiles of 256 of them included
-  return static_cast<int64_t>(r->max_rows) * (nq / c->n_kv_heads) > 0x7fffffff - 256 ? DFLASH_E_SHAPE : DFLASH_OK;
+  // a stream's (row, head of a group) pairs, padded to tiles of 256, are divided by the group in 25 bits
+  return static_cast<int64_t>(r->max_rows) * (nq / c->n_kv_heads) > (1 << 25) - 256 ? DFLASH_E_SHAPE : DFLASH_OK;
 }
 
 // the grid's x axis holds the call's CTAs
@@ -191,8 +191,11 @@ int dflash_page_attention(const dflash_pages* c, const dflash_rows* r, int n_q_h
   a.tile = p.tile;
   a.tile_log2 = log2_of(p.tile);
   a.target = p.target;
+  a.target_inv = static_cast<unsigned>((1ull << 32) / p.target) + 1u;
+  a.group_inv = a.G > 1 ? static_cast<unsigned>((1ull << 32) / a.G) + 1u : 0u;
   a.min_units = p.min_units;
   a.no_split = p.no_split;
+  a.over = p.over;
   a.part_o = p.split ? static_cast<float*>(ws) : nullptr;
   a.part_ml = p.split ? a.part_o + static_cast<size_t>(2 * p.target) * p.tile * c->head_dim : nullptr;
   a.join = p.split ? reinterpret_cast<JoinRecord*>(a.part_ml + static_cast<size_t>(2 * p.target) * p.tile * 2) : nullptr;

@@ -524,7 +524,7 @@ int dflash_page_read(const dflash_pages* pages, const dflash_rows* rows, void* k
  *   out = sum_c softmax_c(scale * <q, k_c>) v_c
  * over the slots c that the row sees; zeros where it sees none. Query heads
  * h * G .. h * G + G - 1 (G = n_q_heads / n_kv_heads, at most
- * DFLASH_MAX_PAGE_GROUP, max_rows * G at most 2^31 - 257) read kv head h.
+ * DFLASH_MAX_PAGE_GROUP, max_rows * G at most 2^25 - 256) read kv head h.
  * A row of stream s, the j-th, sees
  *   - committed slots c < lens[s], and
  *   - of the batch's slots lens[s] + m: CAUSAL: m <= j; BLOCK: all of its
