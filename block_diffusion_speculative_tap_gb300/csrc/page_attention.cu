@@ -774,20 +774,25 @@ PagePlan page_attention_plan(const dflash_pages& c, const dflash_rows& r, int nq
   const bool fp4 = c.format == DFLASH_PAGES_FP4;
   PagePlan p{};
   const int64_t R = static_cast<int64_t>(r.max_rows) * G;
+  // More than 16 (row, head) pairs a kv head go to the tensor-memory kernel: one
+  // 128-row tile for up to 128 pairs, 256-row tiles above. 8 streams x 8192 slots,
+  // 8 kv heads: 32 pairs 57 us there, 75 us in two tiles of 16; 64 pairs 61 and
+  // 167 us (one stream of 4096 slots, 32 pairs: 22 and 16 us). 160 pairs: 75 us
+  // in a 256-row tile, 94 us in two of 128; trees of 372 pairs 115 and 132 us.
   p.tc = c.head_dim >= 64 && R > 16;
   if (p.tc) {
-    p.tile = R > 512 ? 256 : 128;
+    p.tile = R > 128 ? 256 : 128;
     p.unit = 128;
     p.target = 152;
     p.over = 4;
-    p.min_units = 4 + 4;
+    p.min_units = p.over + 4;
     p.no_split = 4;
   } else {
     p.tile = R > 8 ? 16 : 8;
     p.unit = fp4 ? 32 : 16;
     p.target = 152 * (fp4 ? 2 : 1);
     p.over = 8;
-    p.min_units = 8 + 2 * kWarps;
+    p.min_units = p.over + 2 * kWarps;
     p.no_split = 4 * kWarps;
   }
   const int64_t per_stream = (R + p.tile - 1) / p.tile;

@@ -7,11 +7,11 @@
 // the 512). While one stream's four warps turn S into P, the tensor cores work
 // for the other:
 //   pair:   the streams are the halves of a 256-row tile; every K/V tile that
-//           lands in shared memory serves both (prompt chunks, where the
-//           tensor cores are the bound and L2 could not feed one tile each);
+//           lands in shared memory serves both (trees and prompt chunks, where
+//           the tensor cores are the bound and L2 could not feed one tile each);
 //   parity: one 128-row tile, the streams take the even and the odd key tiles
-//           and are joined at the end (blocks and trees, where the cache's
-//           bytes are the bound).
+//           and are joined at the end (blocks, where the cache's bytes are the
+//           bound).
 // A stream's MMAs are issued by one thread in order: S(u+1) behind P(u) V(u), so
 // the completion of scores also says that every earlier output product of the
 // stream is done, and a row's output may be rescaled then. The maximum in use moves only
