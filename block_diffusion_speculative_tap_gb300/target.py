@@ -33,8 +33,6 @@ def _on(index):
     return torch._C._cuda_getCurrentRawStream(index)  # the handle without a Stream object (3 us)
 
 
-
-
 def _like(t):
     """A dense tensor of t's shape and type (t may be strided)."""
     return torch.empty_like(t, memory_format=torch.contiguous_format)
@@ -53,6 +51,8 @@ class Rows:
         self.streams = lens.numel()
         if row_start.numel() != self.streams + 1:
             raise ValueError("row_start: one entry more than lens")
+        if not -0x80000000 <= rows <= 0x7FFFFFFF or not -0x80000000 <= max_rows <= 0x7FFFFFFF:
+            raise ValueError("rows, max_rows: 32-bit numbers")
         if depth is not None and depth.numel() < rows:
             raise ValueError("depth: one entry a row")
         self.rows, self.max_rows = int(rows), int(max_rows)
@@ -172,9 +172,11 @@ class PagedCache:
     def attend(self, rows: Rows, q, window=0, sinks=0, mask="causal", scale=None, out=None, ws=None):
         """dflash_page_attention of q bf16 [rows, n_q, d]. mask: "causal", "block", or
         the rows' mask words int32 [rows, words] (tree_build's node_mask, a row of
-        words a row of the batch). scale: 1 / sqrt(d) unless given. ws: a uint8
+        words a row of the batch). scale: 1 / sqrt(d) unless given. out may be q. ws: a uint8
         workspace of workspace_bytes(); allocated a call unless given."""
         stream = self._check(rows)
+        if max(abs(window), abs(sinks)) > 0x7FFFFFFF:
+            raise ValueError("window, sinks: 32-bit numbers")
         qp, ql, nq = self._rows_of(q, rows, "q")
         mode, mp, mld = A.MASK_TREE, None, 0
         if isinstance(mask, str):

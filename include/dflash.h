@@ -471,8 +471,8 @@ int dflash_tree_verify(int streams, int depth, const int32_t* widths, int vocab,
  * its window starts) is lens[s] + j, or lens[s] + depth[row] where depth is
  * given (a tree's node_depth). row_start ascends from 0 on; max_rows is at
  * least every stream's rows and `rows` at least row_start[streams] (buffers
- * may be longer: rows past the last stream are neither read nor written). A
- * stream may have no rows.
+ * may be longer: what lies in rows past the last stream makes no difference and
+ * stays as it is). A stream may have no rows.
  *
  * What only the device can see wrong is flagged in *status (device int32,
  * DFLASH_STATUS_BAD_PAGE / BAD_ROWS OR-ed in, never cleared; NULL: not
@@ -539,7 +539,7 @@ int dflash_page_read(const dflash_pages* pages, const dflash_rows* rows, void* k
  * 16 slots; a value some row sees has to be finite for the others' sake: a
  * row's weight of zero times an infinity or NaN is NaN.
  *   q, out: device bf16 [rows][n_q_heads][head_dim], rows q_ld / out_ld
- *     elements apart (multiples of 8), 16-byte aligned.
+ *     elements apart (multiples of 8), 16-byte aligned; out may be q.
  *   scale > 0, finite.
  * Scores, softmax and output sums are fp32; the softmax weights enter the
  * second product rounded to bf16 (FP4 pages: to fp16, beside values exact in

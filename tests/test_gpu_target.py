@@ -322,6 +322,91 @@ def test_captured_calls_follow_later_lengths(D, n):
             assert torch.equal(out, st.cache.attend(st.batch, q, window=window, sinks=4)), (lens, window)
 
 
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("n,G", [(1, 4), (16, 4), (40, 8)])
+def test_output_over_the_queries(D, n, G, fp4):
+    st = Setup(D, [n] * 2, [3000, 70], 2, 128, 64, fp4, seed=n)
+    q = st.normal(st.T, 2 * G, 128).to(dev)
+    want = st.cache.attend(st.batch, q)
+    got = q.clone()
+    assert st.cache.attend(st.batch, got, out=got) is got
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("n", [1, 16, 40])
+def test_calls_at_once_on_two_streams(D, n):
+    """Eager calls and captured ones of one cache, on two streams at the same time."""
+    st = Setup(D, [n] * 2, [3000, 900], 2, 128, 64, seed=n)
+    q = st.normal(st.T, 8, 128).to(dev)
+    windows = (0, 600)
+    want = [st.cache.attend(st.batch, q, window=w).clone() for w in windows]
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[], []]
+    for _ in range(25):
+        for i, w in enumerate(windows):
+            with torch.cuda.stream(sides[i]):
+                outs[i].append(st.cache.attend(st.batch, q, window=w))
+    torch.cuda.synchronize()
+    graphs = []
+    for i, w in enumerate(windows):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs[i].append(st.cache.attend(st.batch, q, window=w))
+        graphs.append(g)
+    for _ in range(25):
+        for side, g in zip(sides, graphs):
+            with torch.cuda.stream(side):
+                g.replay()
+    torch.cuda.synchronize()
+    for got, w in zip(outs, want):
+        assert all(torch.equal(o, w) for o in got)
+
+
+@pytest.mark.parametrize("rows,lens,nkv,G", [
+    ([1] * 70, [(37 * i) % 211 for i in range(70)], 2, 2),  # more streams than a warp's lanes
+    ([3] * 40, [(97 * i) % 900 for i in range(40)], 1, 6),
+    ([1, 2], [2900, 10], 40, 1),                            # more kv heads than lanes, split streams
+    ([20, 1], [1500, 3000], 40, 2),
+])
+@pytest.mark.parametrize("fp4", [False, True])
+def test_many_streams_and_many_heads(D, rows, lens, nkv, G, fp4):
+    st = Setup(D, rows, lens, nkv, 64, 16, fp4, seed=len(rows))
+    check_attention(st, st.normal(st.T, nkv * G, 64).to(dev), nkv * G, "causal", window=400, sinks=3)
+
+
+@pytest.mark.parametrize("n", [1, 6])
+def test_rows_far_under_the_bound(D, n):
+    """A padded batch: max_rows and the buffers are for many more rows than there are."""
+    st = Setup(D, [n, 0, n], [300, 5, 1100], 2, 128, 32, seed=n, extra_rows=700)
+    st.batch = D.Rows(st.batch.row_start, st.batch.lens, st.T, 700)
+    q = torch.full((st.T, 8, 128), float("nan"), dtype=torch.bfloat16, device=dev)
+    q[: 2 * n] = st.normal(2 * n, 8, 128).to(dev)
+    out = torch.full_like(q, 7.0)
+    check_attention(st, q, 8, "causal", out=out)
+    assert (out[2 * n :] == 7).all()
+
+
+@pytest.mark.parametrize("n", [1, 9])
+def test_streams_that_share_pages(D, n):
+    """A common prompt: the committed pages of one stream in another's table."""
+    st = Setup(D, [n, n], [128, 128], 2, 64, 16, seed=n)
+    st.table[1, :8] = st.table[0, :8]
+    st.k_val[1][:128], st.v_val[1][:128] = st.k_val[0][:128], st.v_val[0][:128]
+    check_attention(st, st.normal(st.T, 8, 64).to(dev), 8, "causal")
+
+
+def test_numbers_past_32_bits_are_refused(D):
+    st = Setup(D, [1], [20], 2, 64, 16)
+    q = st.normal(1, 4, 64).to(dev)
+    for bad in (dict(window=1 << 32), dict(window=(1 << 32) + 5), dict(window=4, sinks=1 << 31)):
+        with pytest.raises(ValueError):
+            st.cache.attend(st.batch, q, **bad)
+    for n, m in ((1 << 32, 1), (1, 1 << 32), (-(1 << 32), 1)):
+        with pytest.raises(ValueError):
+            D.Rows(st.batch.row_start, st.batch.lens, n, m)
+
+
 def test_bad_tables_and_rows_are_flagged_and_never_followed(D):
     """A needed slot without a page, lengths past the table, descending row_start:
     status bits, rows of other streams unharmed."""
@@ -578,6 +663,17 @@ def test_token_counts(D):
     for s in range(S):
         O.count_tokens(want[s], rows[s], False)
     assert np.array_equal(counts.cpu().numpy().view(np.uint16), want)
+
+
+def test_rules_of_more_streams_than_a_grid_axis_holds(D):
+    S, V = 65600, 8
+    g = torch.Generator().manual_seed(4)
+    x = torch.randn(S, 1, V, generator=g).to(torch.bfloat16).to(dev)
+    counts = torch.randint(0, 3, (S, V), generator=g).to(torch.int16).to(dev)
+    presence = torch.randn(S, generator=g).to(dev)
+    got = D.logit_rules(x, counts=counts, presence=presence)
+    want = torch.where(counts[:, None] > 0, x.float() - presence[:, None, None], x.float()).to(torch.bfloat16)
+    assert torch.equal(got, want)
 
 
 # ---------------------------------------------------------------- the pass as it is used
