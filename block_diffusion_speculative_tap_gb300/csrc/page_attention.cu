@@ -25,6 +25,12 @@
 // Few rows and long caches: CTAs take equal shares of all streams' keys (see
 // Share), a part's (m, l, O) goes to the workspace and page_combine_kernel
 // joins a row's parts.
+//
+// Bound by the cache's bytes where there are many (32 tokens in windows of 2048,
+// 8 kv heads of 128: 48.5 us, 5.4 TB/s), by latency for one stream (4096 slots:
+// 11.6 us for 16.8 MB), and over 4-bit pages by issue slots: a value costs about
+// two instructions from its code to the MMA (32 tokens over 1 to 16 k slots: 86
+// us, 3.8 TB/s).
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -613,8 +619,8 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
 // CTA a boundary (and rows of its tile).
 //
 // Tiles of up to 16 rows: a warp a row, kAhead parts loaded before any is used
-// (a token of 8 kv heads over all SMs is 19 parts of few rows: 15.4 -> 12.8 us
-// a call).
+// (a token of 8 kv heads over all SMs is 19 parts of few rows: a call took 15.4
+// us with a part at a time, 12.8 us with all in flight).
 constexpr int kCombineRows = 8;
 constexpr int kAhead = 20;
 template <int D>
@@ -730,7 +736,7 @@ __global__ void __launch_bounds__(D * 4) page_combine_tile_kernel(const __grid_c
                  pack2(acc[4] * inv, acc[5] * inv, false), pack2(acc[6] * inv, acc[7] * inv, false));
 }
 
-// A kernel's shared-memory limit, raised once a device.
+// A kernel's shared-memory limit (of the current device).
 int raise_smem(const void* kern, int bytes) {
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess ? DFLASH_OK
                                                                                                        : DFLASH_E_CUDA;
@@ -783,14 +789,14 @@ PagePlan page_attention_plan(const dflash_pages& c, const dflash_rows& r, int nq
   if (p.tc) {
     p.tile = R > 128 ? 256 : 128;
     p.unit = 128;
-    p.target = 152;
-    p.over = 4;
+    p.target = 152;  // a CTA an SM
+    p.over = 4;      // a segment's start and end cost about four key tiles
     p.min_units = p.over + 4;
     p.no_split = 4;
   } else {
     p.tile = R > 8 ? 16 : 8;
     p.unit = fp4 ? 32 : 16;
-    p.target = 152 * (fp4 ? 2 : 1);
+    p.target = 152 * (fp4 ? 2 : 1);  // CTAs resident at once
     p.over = 8;
     p.min_units = p.over + 2 * kWarps;
     p.no_split = 4 * kWarps;
