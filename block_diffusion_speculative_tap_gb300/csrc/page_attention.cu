@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kWarps * 32, FP4 ? 2 : 1) page_attn_kernel(con
   pdl_wait();
   pdl_trigger();
   for (bool first = true;; first = false) {
-  if (warp == 0) run_next(a, &run, first);
+  if (warp == 0) run_next<D == 32>(a, &run, first);  // (more rows of longer heads go to the tensor-memory kernel)
   __syncthreads();
   if (!run.left) {
     if (first && threadIdx.x == 0) write_join(a, run);
@@ -805,8 +805,9 @@ PagePlan page_attention_plan(const dflash_pages& c, const dflash_rows& r, int nq
   const int64_t by_rows = (static_cast<int64_t>(r.rows) * G + p.tile - 1) / p.tile + c.streams;
   const int64_t tiles = std::min(c.streams * per_stream, by_rows) * c.n_kv_heads;
   const int64_t units = (static_cast<int64_t>(c.table_cols) * c.page_size + p.unit - 1) / p.unit;
-  // (places on the line of all units are 31 bits wide)
-  p.split = units > p.no_split && c.streams * per_stream * c.n_kv_heads < 0x7fffffff / (units + p.over);
+  // (places on the line of all units, rows past the table's end among them, are 31 bits wide)
+  p.split = units > p.no_split &&
+            c.streams * per_stream * c.n_kv_heads < 0x7fffffff / (units + r.max_rows / p.unit + 1 + p.over);
   p.ctas = std::max<int64_t>(tiles, p.split ? p.target : 0);
   return p;
 }

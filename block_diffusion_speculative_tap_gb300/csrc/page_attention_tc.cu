@@ -28,9 +28,9 @@
 // bounded.
 //
 // Measured, heads of 128, 8 kv heads: blocks (8 streams of 16 rows, 40 heads,
-// 8192 slots, parity) 60.6 us, 4.5 TB/s: the cache's bytes take 45 us of it;
-// trees (6 of 93 nodes, 32 heads, 1 to 16 k slots, pair) 115.5 us, 709 TFLOP/s; a
-// prompt chunk (4096 rows over 4096 slots, 32 heads, pair) 376 us, 1098 TFLOP/s,
+// 8192 slots, parity) 61 us, 4.5 TB/s: the cache's bytes take 45 us of it;
+// trees (6 of 93 nodes, 32 heads, 1 to 16 k slots, pair) 115 us, 713 TFLOP/s; a
+// prompt chunk (4096 rows over 4096 slots, 32 heads, pair) 350 us, 1178 TFLOP/s,
 // bound by the issuing thread; 4-bit blocks (9 of 16 rows, 40 heads, 4 to 16 k
 // slots, parity) 70 us, bound by the conversion's and the softmax's latency.
 #include <cuda_fp16.h>
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
   for (bool first = true;; first = false) {
   // between segments everything asynchronous has completed: the barriers start
   // again at phase 0
-  if (warp == 0) run_next(a, run, first);
+  if (warp == 0) run_next<PAIR>(a, run, first);
   if (first && warp == kMma) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();

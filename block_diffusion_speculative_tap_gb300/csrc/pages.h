@@ -98,8 +98,11 @@ __device__ __forceinline__ UnitRange unit_range(int lo, int hi, int sinks, int u
 // n rows is mt tiles of `tile` (row, head) pairs; a tile's keys are the
 // stream's units. All tiles' units, kv head by kv head, stream by stream, make
 // one line, and CTA b takes the part [b * per, (b + 1) * per) of it: streams of
-// unequal length make equal shares. A tile's place on the line begins with
-// `over` units that stand for what a segment costs beside its keys; a boundary
+// unequal length make equal shares. Tiles of a prompt's causal rows see ever
+// more units, so they lie in pairs of the longest left and the shortest left,
+// whose places add up to the same for every pair (2500 rows over 4096 slots, 32
+// heads: 234 us with places as long as the longest, 203 us so). A tile's place on the
+// line begins with `over` units that stand for what a segment costs beside its keys; a boundary
 // that falls on them is one at the tile's start. A share is a run of segments,
 // each (part of) one tile; a part goes to the workspace, slot 2b for a CTA's first segment
 // and 2b + 1 for its last, and the combine kernels join the parts. With many
@@ -136,13 +139,35 @@ struct Run {
   Segment seg;
 };
 
-// A lane's stream: its rows, tiles and units.
+// n / G for n under 2^25 (group_inv: 2^32 / G rounded up; 0 for G = 1).
+__device__ __forceinline__ int by_group(const PageAttnArgs& a, unsigned n) {
+  return static_cast<int>(a.group_inv ? __umulhi(n, a.group_inv) : n);
+}
+
+// MANY below: streams may have more than one tile. Kernels that never see such a
+// call are compiled without what only it needs: all of this starts from a cold
+// instruction cache (4-bit blocks of 80 pairs: 72 us with it, 70 us without).
+
+// Whether the tiles of a stream differ in length: by a constant from each to the
+// next, up to rounding.
+__device__ __forceinline__ bool rising(const PageAttnArgs& a) {
+  return a.mode == DFLASH_MASK_CAUSAL && a.window == 0;
+}
+// Length of such a tile's place on the line.
+__device__ __forceinline__ int rising_place(const PageAttnArgs& a, const StreamRows& q, int tile) {
+  const int j_hi = min(q.n - 1, by_group(a, (static_cast<unsigned>(tile + 1) << a.tile_log2) - 1u));
+  return unit_range(0, q.C + j_hi + 1, 0, a.unit_log2).n + a.over;
+}
+
+// A lane's stream: its rows, tiles, the place of its longest tile, of two (the
+// longest and the shortest), and of all on the line.
 struct LaneStream {
   StreamRows q;
-  int mt, u;
+  int mt, u, two, all;
 };
+template <bool MANY>
 __device__ __forceinline__ LaneStream lane_stream(const PageAttnArgs& a, int s, bool flag) {
-  LaneStream x{{0, 0, 0}, 0, 0};
+  LaneStream x{{0, 0, 0}, 0, 0, 0, 0};
   if (s >= a.r.S) return x;
   bool bad;
   x.q = stream_rows(a.r, s, &bad);
@@ -151,24 +176,49 @@ __device__ __forceinline__ LaneStream lane_stream(const PageAttnArgs& a, int s, 
   x.mt = (x.q.n * a.G + (1 << a.tile_log2) - 1) >> a.tile_log2;  // max_rows * G is under 2^31
   const int lo = a.window > 0 ? max(0, x.q.C - a.window + 1) : 0;
   x.u = unit_range(lo, x.q.C + x.q.n, a.sinks, a.unit_log2).n + a.over;
+  x.two = 2 * x.u;
+  x.all = x.mt * x.u;
+  if (MANY && x.mt > 1) {
+    if (rising(a)) {
+      x.two = x.u + rising_place(a, x.q, 0);
+      x.all = (x.mt >> 1) * x.two + ((x.mt & 1) ? rising_place(a, x.q, x.mt >> 1) : 0);
+    } else if (a.mode == DFLASH_MASK_CAUSAL && a.r.depth == nullptr) {
+      // a window moves on through the chunk with a tile's rows (4096 rows in a window of
+      // 1000: 189 us when tiles went back to the chunk's start, 121 us so)
+      const int more = (1 << a.unit_log2) - 1;
+      const int reach = min(a.window, 0x3fffffff) + by_group(a, 1u << a.tile_log2) + 1;
+      x.u = min(x.u, ((reach + more) >> a.unit_log2) + 1 + ((min(a.sinks, 0x3fffffff) + more) >> a.unit_log2) + a.over);
+      x.two = 2 * x.u;
+      x.all = x.mt * x.u;
+    }
+  }
   return x;
 }
 
 // One warp; every lane gets the answer. `last`: the lanes' streams when there
 // are no more than 32 of them.
+template <bool MANY>
 __device__ __forceinline__ Share share_of(const PageAttnArgs& a, LaneStream& last) {
   const int lane = threadIdx.x & 31;
   unsigned line = 0, tiles = 0;
-  int most = 0;
+  int most = 0, least = MANY ? 0x7fffffff : 0;
   for (int s0 = 0; s0 < a.r.S; s0 += 32) {
-    last = lane_stream(a, s0 + lane, blockIdx.x == 0 && blockIdx.y == 0);
-    line += __reduce_add_sync(0xffffffffu, static_cast<unsigned>(last.mt * last.u));
+    last = lane_stream<MANY>(a, s0 + lane, blockIdx.x == 0 && blockIdx.y == 0);
+    line += __reduce_add_sync(0xffffffffu, static_cast<unsigned>(last.all));
     tiles += __reduce_add_sync(0xffffffffu, static_cast<unsigned>(last.mt));
     most = max(most, __reduce_max_sync(0xffffffffu, last.u));
+    if (MANY)
+      least = min(least, __reduce_min_sync(0xffffffffu, last.mt ? last.two - last.u : 0x7fffffff));
   }
   Share sh;
   const unsigned all = tiles * a.c.nkv;
-  sh.whole = a.part_o == nullptr || most <= a.no_split + a.over || all >= 3u * a.target;
+  // Three tiles a CTA and more are taken whole, and twelve where the tensor cores
+  // are the bound (256-row tiles) and even the shortest tile is long: a chunk of 4096 rows
+  // over 4096 slots 350 us split, 375 whole, over 20000 slots 1095 and 1229; 6000
+  // rows over none, whose last tiles are short, 297 and 275; 60 blocks of 4000
+  // slots, bound by their bytes, 264 and 254.
+  const unsigned many = a.tile > 128 && least >= a.over + 24 ? 12u : 3u;
+  sh.whole = a.part_o == nullptr || most <= a.no_split + a.over || all >= many * a.target;
   sh.line = static_cast<int>(sh.whole ? tiles : line);
   sh.total = sh.line * a.c.nkv;
   // more than total / target (target_inv > 2^32 / target), so that no CTA past the target has work
@@ -177,17 +227,13 @@ __device__ __forceinline__ Share share_of(const PageAttnArgs& a, LaneStream& las
   return sh;
 }
 
-// n / G for n under 2^25 (group_inv: 2^32 / G rounded up; 0 for G = 1).
-__device__ __forceinline__ int by_group(const PageAttnArgs& a, unsigned n) {
-  return static_cast<int>(a.group_inv ? __umulhi(n, a.group_inv) : n);
-}
-
 __device__ __forceinline__ int row_pos(const RowsArgs& r, const StreamRows& q, int j) {
   return q.C + (r.depth ? max(0, min(r.depth[q.row0 + j], 0x3fffffff)) : j);
 }
 
 // The segment at place `at` of the line, `left` units (whole: a tile) at most.
 // One warp; false past the end. known: the lanes' streams, if they are at hand.
+template <bool MANY>
 __device__ __forceinline__ bool segment_at(const PageAttnArgs& a, const Share& sh, int at, int left,
                                            bool have, const LaneStream& known, Segment* out, int* next) {
   const int lane = threadIdx.x & 31;
@@ -208,8 +254,8 @@ __device__ __forceinline__ bool segment_at(const PageAttnArgs& a, const Share& s
   }
   int base = 0;
   for (int s0 = 0; s0 < a.r.S; s0 += 32) {
-    const LaneStream x = have ? known : lane_stream(a, s0 + lane, false);
-    const int cnt = sh.whole ? x.mt : x.mt * x.u;
+    const LaneStream x = have ? known : lane_stream<MANY>(a, s0 + lane, false);
+    const int cnt = sh.whole ? x.mt : x.all;
     int inc = cnt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -229,15 +275,28 @@ __device__ __forceinline__ bool segment_at(const PageAttnArgs& a, const Share& s
     g.q.n = __shfl_sync(0xffffffffu, x.q.n, l);
     g.q.C = __shfl_sync(0xffffffffu, x.q.C, l);
     const int tiles = __shfl_sync(0xffffffffu, x.mt, l);
-    const int tile = sh.whole ? rel
-                     : tiles == 1 ? 0
-                                  : static_cast<int>(static_cast<unsigned>(rel) / static_cast<unsigned>(g.u));
-    g.x0 = sh.whole ? 0 : rel - tile * g.u;
+    g.tile = tiles - 1;
+    g.x0 = 0;
+    if (sh.whole) {  // the last rows see most: start with them
+      g.tile -= rel;
+    } else if (!MANY || tiles == 1) {
+      g.x0 = rel;
+    } else {
+      const int two = __shfl_sync(0xffffffffu, x.two, l);
+      const int pair = static_cast<int>(static_cast<unsigned>(rel) / static_cast<unsigned>(two));
+      g.tile -= pair;
+      g.x0 = rel - pair * two;
+      if (rising(a)) g.u = rising_place(a, g.q, g.tile);
+      if (g.x0 >= g.u) {  // the pair's other tile (one in the middle has none)
+        g.x0 -= g.u;
+        g.u = two - g.u;
+        g.tile = pair;
+      }
+    }
     g.x1 = sh.whole ? g.u : min(g.u, g.x0 + left);
     *next = at + (sh.whole ? 1 : g.x1 - g.x0);
     if (g.x1 < g.u && g.x1 <= a.over) return false;  // the next CTA's from the start
     if (g.x0 <= a.over) g.x0 = 0;
-    g.tile = tiles - 1 - tile;  // the last rows see most: whole tiles start with them
     const unsigned f0 = static_cast<unsigned>(g.tile) << a.tile_log2;
     g.j_lo = by_group(a, f0);
     g.j_hi = min(g.q.n - 1, by_group(a, f0 + (1u << a.tile_log2) - 1u));
@@ -257,13 +316,22 @@ __device__ __forceinline__ bool segment_at(const PageAttnArgs& a, const Share& s
         p_lo = __reduce_min_sync(0xffffffffu, p_lo);
         p_hi = __reduce_max_sync(0xffffffffu, p_hi);
       }
-      g.lo = min(g.q.C, max(0, p_lo - a.window + 1));
+      // (with depths the batch's slots are not in the order of their positions)
+      g.lo = min(a.r.depth ? g.q.C : g.hi, max(0, p_lo - a.window + 1));
       g.lo_max = max(0, p_hi - a.window + 1);
     }
     g.ur = unit_range(g.lo, g.hi, a.sinks, a.unit_log2);
-    // a tile sees no more units than its stream: the rest of a part is empty
-    g.i0 = min(max(g.x0 - a.over, 0), g.ur.n);
-    g.i1 = g.x1 == g.u ? g.ur.n : min(g.x1 - a.over, g.ur.n);
+    g.i0 = max(g.x0 - a.over, 0);
+    g.i1 = g.x1 - a.over;
+    if (MANY && g.ur.n != g.u - a.over) {
+      // the tile's units, as many as they are, spread evenly over its place
+      const float rate = __fdividef(static_cast<float>(g.ur.n), static_cast<float>(g.u - a.over));
+      g.i0 = static_cast<int>(static_cast<float>(g.i0) * rate);
+      g.i1 = static_cast<int>(static_cast<float>(g.i1) * rate);
+    }
+    // (one tile may see fewer units than its place has: the rest of a part is empty)
+    g.i0 = min(g.i0, g.ur.n);
+    g.i1 = g.x1 == g.u ? g.ur.n : min(g.i1, g.ur.n);
     *out = g;
     return true;
   }
@@ -271,13 +339,14 @@ __device__ __forceinline__ bool segment_at(const PageAttnArgs& a, const Share& s
 }
 
 // The CTA's next segment into run->seg. One warp.
+template <bool MANY>
 __device__ __forceinline__ void run_next(const PageAttnArgs& a, Run* run, bool begin) {
   const bool one = (threadIdx.x & 31) == 0;
   Share sh;
-  LaneStream x{{0, 0, 0}, 0, 0};
+  LaneStream x{{0, 0, 0}, 0, 0, 0, 0};
   int at = 0, end = 0;
   if (begin) {
-    sh = share_of(a, x);
+    sh = share_of<MANY>(a, x);
     at = sh.start(static_cast<int>(blockIdx.x));
     end = sh.start(static_cast<int>(blockIdx.x) + 1);
     if (one) {
@@ -291,7 +360,7 @@ __device__ __forceinline__ void run_next(const PageAttnArgs& a, Run* run, bool b
   }
   Segment g;
   int next = at;
-  const bool left = at < end && segment_at(a, sh, at, end - at, begin && a.r.S <= 32, x, &g, &next);
+  const bool left = at < end && segment_at<MANY>(a, sh, at, end - at, begin && a.r.S <= 32, x, &g, &next);
   __syncwarp();
   if (one) {
     run->left = left;

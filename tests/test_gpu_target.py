@@ -375,6 +375,18 @@ def test_many_streams_and_many_heads(D, rows, lens, nkv, G, fp4):
     check_attention(st, st.normal(st.T, nkv * G, 64).to(dev), nkv * G, "causal", window=400, sinks=3)
 
 
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (90, 5), (300, 0), (900, 200)])
+@pytest.mark.parametrize("rows,lens,nkv,G", [([700, 5, 333], [1000, 900, 0], 1, 3), ([97], [2000], 2, 8), ([1025], [0], 1, 1),
+                                             ([16, 15], [800, 3000], 1, 1)])
+@pytest.mark.parametrize("depths", [False, True])
+def test_prompt_chunks(D, rows, lens, nkv, G, window, sinks, depths):
+    """Rows of several tiles, whose tiles see more and more (or a window that moves on
+    through the chunk itself), split over CTAs."""
+    depth = [j + (j * 7) % 5 for n in rows for j in range(n)] if depths else None
+    st = Setup(D, rows, lens, nkv, 64, 32, seed=sum(rows), depth=depth)
+    check_attention(st, st.normal(st.T, nkv * G, 64).to(dev), nkv * G, "causal", window, sinks)
+
+
 @pytest.mark.parametrize("n", [1, 6])
 def test_rows_far_under_the_bound(D, n):
     """A padded batch: max_rows and the buffers are for many more rows than there are."""
