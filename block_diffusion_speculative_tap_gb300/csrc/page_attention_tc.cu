@@ -614,8 +614,10 @@ __global__ void __launch_bounds__((TcGeo<D, FP4, PAIR>::kThreads), 1)
       // thread would have to commit once more.)
       if (q4 == 0 && lane == 0) {
         const int t = tile_of(s, u), tv = PAIR ? t - 1 : t - 2;
-        mbar_arrive(&empty[slot_of(0, t)]);
+        // V first: a producer that finds K's slot free may ask next for the slot that
+        // V's is the turn before last of, and take that phase for the one before.
         if (tv >= 0) mbar_arrive(&empty[slot_of(1, tv)]);
+        mbar_arrive(&empty[slot_of(0, t)]);
       }
       if (idle) {
         if (lane == 0) mbar_arrive(&p_full[s]);
