@@ -2,13 +2,17 @@
 K/V cache, its attention and the logit rules of include/dflash.h.
 
 Tensors are checked for type, device and layout here; shapes and limits are
-checked by the library. Workspaces are allocated a call on the current stream,
-so calls on several streams, and captured graphs, never share one.
+checked by the library. The attention's workspace is kept for each thread and
+stream and grows to the largest asked for (a call's allocation cost 4 us of 18);
+a captured call gets one of its own from the graph's pool. So calls that may
+overlap, on several streams, from several threads or in captured graphs, never
+share one.
 """
 from __future__ import annotations
 
 import ctypes as C
 import math
+import threading
 
 import torch
 
@@ -31,6 +35,24 @@ def _on(index):
     if index < 0 or index != torch.cuda.current_device():
         raise ValueError("expected tensors on the current CUDA device")
     return torch._C._cuda_getCurrentRawStream(index)  # the handle without a Stream object (3 us)
+
+
+_kept = threading.local()
+
+
+def _workspace(nbytes, device, index, stream):
+    """A pointer to nbytes for one call on the device's current stream, and their owner."""
+    if torch._C._cuda_isCurrentStreamCapturing():
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return ws.data_ptr(), ws
+    spaces = _kept.__dict__
+    key = (index, stream)
+    ptr, size, ws = spaces.get(key, (None, 0, None))
+    if size < nbytes:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)  # (the old one goes back to this stream's pool)
+        ptr = ws.data_ptr()
+        spaces[key] = (ptr, nbytes, ws)
+    return ptr, ws
 
 
 def _like(t):
@@ -173,7 +195,7 @@ class PagedCache:
         """dflash_page_attention of q bf16 [rows, n_q, d]. mask: "causal", "block", or
         the rows' mask words int32 [rows, words] (tree_build's node_mask, a row of
         words a row of the batch). scale: 1 / sqrt(d) unless given. out may be q. ws: a uint8
-        workspace of workspace_bytes(); allocated a call unless given."""
+        workspace of workspace_bytes(), for this call alone; kept by the stream unless given."""
         stream = self._check(rows)
         if max(abs(window), abs(sinks)) > 0x7FFFFFFF:
             raise ValueError("window, sinks: 32-bit numbers")
@@ -194,8 +216,8 @@ class PagedCache:
             op, ol, _ = self._rows_of(out, rows, "out", nq)
         if ws is None:
             nbytes = self.workspace_bytes(rows, nq)
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device) if nbytes else None
-            wp, wn = (ws.data_ptr(), nbytes) if nbytes else (None, 0)
+            wp, ws = _workspace(nbytes, self.device, self.index, stream) if nbytes else (None, None)
+            wn = nbytes
         else:
             wp, wn = _need(ws, torch.uint8, self.device, "ws"), ws.numel()
         check(
@@ -251,7 +273,7 @@ def logit_rules(logits, counts=None, tokens=None, node_mask=None, repetition=Non
     def opt(t, dtype, shape, what):
         if t is None:
             return None
-        if tuple(t.shape) != shape:
+        if t.shape != shape:
             raise ValueError(f"{what}: expected {list(shape)}, got {list(t.shape)}")
         return _need(t, dtype, dev, what)
 

@@ -408,6 +408,51 @@ def test_streams_that_share_pages(D, n):
     check_attention(st, st.normal(st.T, 8, 64).to(dev), 8, "causal")
 
 
+def test_threads_on_one_stream(D):
+    """Two threads' calls on one stream, in whatever order their launches come."""
+    import threading
+
+    setups = [Setup(D, [n] * 2, [3000, 900], 2, 128, 64, seed=n) for n in (16, 40)]
+    qs = [st.normal(st.T, 8, 128).to(dev) for st in setups]
+    want = [st.cache.attend(st.batch, q).clone() for st, q in zip(setups, qs)]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        for _ in range(100):
+            got[i].append(setups[i].cache.attend(setups[i].batch, qs[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for outs, w in zip(got, want):
+        assert len(outs) == 100 and all(torch.equal(o, w) for o in outs)
+
+
+def test_a_workspace_that_grows(D):
+    """Small, large and small calls again, eager and captured, one behind the other."""
+    small, large = (Setup(D, [n], [2000], 2, 128, 64, seed=n) for n in (1, 60))
+    q0, q1 = small.normal(1, 8, 128).to(dev), large.normal(60, 8, 128).to(dev)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        a = small.cache.attend(small.batch, q0)
+        b = large.cache.attend(large.batch, q1)
+        c = small.cache.attend(small.batch, q0)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        d = large.cache.attend(large.batch, q1)
+        e = small.cache.attend(small.batch, q0)
+    for _ in range(3):
+        g.replay()
+        f = large.cache.attend(large.batch, q1)
+        torch.cuda.synchronize()
+        assert torch.equal(a, c) and torch.equal(a, e) and torch.equal(b, d) and torch.equal(b, f)
+
+
 def test_numbers_past_32_bits_are_refused(D):
     st = Setup(D, [1], [20], 2, 64, 16)
     q = st.normal(1, 4, 64).to(dev)
